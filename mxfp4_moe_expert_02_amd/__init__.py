@@ -2,7 +2,8 @@
 
 The layer itself is hand-written HIP in ``csrc/`` behind the C ABI of
 ``include/moe_mxfp4.h``, built into ``libmoe_mxfp4.so`` by ``build.py``.
-``_lib`` is the ctypes binding (same names as the C ABI); ``layer`` builds a
+``_lib`` is the ctypes binding (same names as the C ABI); ``_ops`` that of the
+operators around the layer (``include/ops/moe_ops.h``); ``layer`` builds a
 device-resident synthetic layer for tests and benchmarks.
 """
 from ._lib import (MOE_ACT_BF16, MOE_ACT_MXFP8, MOE_DT_BF16, MOE_DT_F32, MOE_DT_I32, MOE_DT_U8,
@@ -19,5 +20,8 @@ from ._lib import (MOE_ACT_BF16, MOE_ACT_MXFP8, MOE_DT_BF16, MOE_DT_F32, MOE_DT_
                    moe_mxfp8_quantize, moe_probe_copy,
                    moe_probe_read_cached, moe_probe_sink_words, moe_probe_stream_read,
                    tensor_desc)
+from ._ops import (MOE_EPI_GELU, MOE_EPI_NONE, MOE_EPI_SILU, MOE_EPI_SILU_MUL, moe_combine,
+                   moe_combine_backward, moe_dispatch, moe_dispatch_backward, moe_dispatch_workspace,
+                   moe_mxfp8_linear, moe_mxfp8_linear_workspace, moe_rmsnorm)
 
 __all__ = [n for n in dir() if n.startswith(("moe_", "MOE_"))] + ["MoeError", "lib", "tensor_desc"]

@@ -27,7 +27,9 @@ CFLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 
 
 def sources() -> list[str]:
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
+    """The layer's sources (csrc/) and those of the operators around it (csrc/ops/)."""
+    dirs = (CSRC, os.path.join(CSRC, "ops"))
+    return sorted(os.path.join(d, f) for d in dirs for f in os.listdir(d) if f.endswith(".hip"))
 
 
 def _compile(src: str, bdir: str, extra: list) -> str:

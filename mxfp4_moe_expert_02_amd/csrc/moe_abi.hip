@@ -25,6 +25,7 @@
 
 namespace {
 
+using moe::hip_fail;
 using moe::Workspace;
 
 constexpr int kMaxDevices = 64;
@@ -32,11 +33,6 @@ Workspace* g_ws[kMaxDevices] = {};
 int g_num_ws = 0;  // number of live workspaces (0: nothing initialised)
 std::mutex g_mu;
 thread_local char g_hip_msg[256] = "";
-
-int hip_fail(hipError_t err, const char* what) {
-    snprintf(g_hip_msg, sizeof(g_hip_msg), "%s: %s (%d)", what, hipGetErrorString(err), (int)err);
-    return MOE_E_HIP;
-}
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -157,6 +153,11 @@ hipError_t na_scratch(uint8_t** p) {
 }  // namespace
 
 namespace moe {
+
+int hip_fail(hipError_t err, const char* what) {
+    snprintf(g_hip_msg, sizeof(g_hip_msg), "%s: %s (%d)", what, hipGetErrorString(err), (int)err);
+    return MOE_E_HIP;
+}
 
 hipError_t resident_grid(const void* kernel, int block, int* grid) {
     int dev = 0, cus = 0, per_cu = 0;

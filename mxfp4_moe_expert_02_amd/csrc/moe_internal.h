@@ -215,6 +215,10 @@ struct GemmArgs {
     int sh_row0;
 };
 
+// Keeps the text of a failed HIP call for moe_mxfp4_status_string (calling
+// thread) and returns MOE_E_HIP (moe_abi.hip)
+int hip_fail(hipError_t err, const char* what);
+
 // ---------------------------------------------------------------- launchers
 // Workgroups of `kernel` (block threads, static LDS only) that fit on the
 // current device at once: occupancy per CU x CUs.

@@ -1,0 +1,163 @@
+// rmsnorm.hip -- residual addition, RMS norm and MXFP8 encoding in one pass.
+//
+//   s = x + residual,  n = s * weight / sqrt(mean(s^2) + eps)
+//
+// One workgroup owns a row and holds it in registers: every thread loads
+// its pieces of 8 elements (16 bytes of bf16), adds the residual, writes
+// the sum back, squares it into the row's sum (one cross-lane and one LDS
+// reduction), and then scales and encodes what it still holds.  A row is
+// read once and written once; the kernel is bound by those bytes.
+//
+// Everything between the loads and the roundings is in 64 bits, where the
+// vector ALU of gfx950 runs as many multiply-adds per clock as in (unpacked)
+// 32: about 16 operations per element.  The 8-bit codes are a decision on n,
+// and a float32 n takes it differently about once per million elements;
+// here the codes are the formula's.
+#include "ops_internal.h"
+
+namespace moe {
+namespace {
+
+__device__ inline double wave_sum(double v) {
+#pragma unroll
+    for (int m = 1; m < kWave; m <<= 1) v += __shfl_xor(v, m);
+    return v;
+}
+
+// v with its low word folded into the last bit of the high one (set if any
+// low bit is): 21 significant bits that a later rounding to 8 bits takes
+// for the whole value, exact in float32 over float32's range.
+__device__ inline double sticky(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t hi = (uint32_t)(b >> 32) | (uint32_t)((uint32_t)b != 0);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32);
+}
+
+// double -> bf16, one rounding: the sticky form holds every bit that
+// matters and float32's rounding to bf16 sees a tie only where there is one
+__device__ inline float to_f32_odd(double v) { return (float)sticky(v); }
+
+constexpr int kNormPiece = 8;
+
+// WPR: waves per row, 1 (four rows per workgroup of 256 threads) or more
+// (one row per workgroup); NP: pieces of 8 elements per thread.
+template <typename X, typename R, int WPR, int NP>
+__global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR)
+rmsnorm_kernel(moe_rmsnorm_args a) {
+    constexpr int kThreads = 64 * WPR;  // of a row
+    __shared__ double part[WPR];
+    const int tid = WPR == 1 ? threadIdx.x % 64 : threadIdx.x;
+    const int64_t t = WPR == 1 ? (int64_t)blockIdx.x * 4 + threadIdx.x / 64 : (int64_t)blockIdx.x;
+    if (t >= a.num_tokens) return;  // WPR == 1 only: whole waves, no barrier below
+    const int H = (int)a.hidden, pieces = H / kNormPiece;
+    const X* x = (const X*)a.x + t * a.x_stride;
+    const R* r = a.residual ? (const R*)a.residual + t * a.residual_stride : nullptr;
+    R* ro = a.residual_out ? (R*)a.residual_out + t * a.residual_out_stride : nullptr;
+    // every load of the row is issued before the first store (the outputs may
+    // be the inputs, so the compiler keeps loads behind stores)
+    float xv[NP][kNormPiece], rv[NP][kNormPiece], wv[NP][kNormPiece];
+#pragma unroll
+    for (int p = 0; p < NP; p++) {
+        const int i = p * kThreads + tid;
+#pragma unroll
+        for (int e = 0; e < kNormPiece; e++) xv[p][e] = rv[p][e] = wv[p][e] = 0.f;
+        if (i < pieces) {
+            load_piece<kNormPiece>(x + i * kNormPiece, xv[p]);
+            if (r) load_piece<kNormPiece>(r + i * kNormPiece, rv[p]);
+            if (a.weight_dtype == MOE_DT_F32)
+                load_piece<kNormPiece>((const float*)a.weight + i * kNormPiece, wv[p]);
+            else
+                load_piece<kNormPiece>((const uint16_t*)a.weight + i * kNormPiece, wv[p]);
+        }
+    }
+    double s[NP][kNormPiece];
+    double sum = 0.0;
+#pragma unroll
+    for (int p = 0; p < NP; p++)
+#pragma unroll
+        for (int e = 0; e < kNormPiece; e++) {
+            s[p][e] = r ? (double)xv[p][e] + (double)rv[p][e] : (double)xv[p][e];
+            sum = fma(s[p][e], s[p][e], sum);
+        }
+    if (ro) {
+#pragma unroll
+        for (int p = 0; p < NP; p++) {
+            const int i = p * kThreads + tid;
+            float o[kNormPiece];
+#pragma unroll
+            for (int e = 0; e < kNormPiece; e++) o[e] = sizeof(R) == 2 ? to_f32_odd(s[p][e]) : (float)s[p][e];
+            if (i < pieces) store_piece<kNormPiece>(ro + i * kNormPiece, o);
+        }
+    }
+    sum = wave_sum(sum);
+    if constexpr (WPR > 1) {
+        if (tid % kWave == 0) part[tid / kWave] = sum;
+        __syncthreads();
+        sum = 0.0;
+#pragma unroll
+        for (int w = 0; w < WPR; w++) sum += part[w];
+    }
+    const double rinv = 1.0 / sqrt(sum / H + a.eps);
+    uint16_t* y = a.y ? (uint16_t*)a.y + t * a.y_stride : nullptr;
+#pragma unroll
+    for (int p = 0; p < NP; p++) {
+        const int i = p * kThreads + tid;
+        const bool live = i < pieces;
+        double n[kNormPiece];
+#pragma unroll
+        for (int e = 0; e < kNormPiece; e++) n[e] = s[p][e] * (double)wv[p][e] * rinv;
+        if (y && live) {
+            float o[kNormPiece];
+#pragma unroll
+            for (int e = 0; e < kNormPiece; e++) o[e] = to_f32_odd(n[e]);
+            store_piece<kNormPiece>(y + i * kNormPiece, o);
+        }
+        if (!a.codes) continue;
+        // a block of 32 lies in four neighbouring lanes, which agree on its
+        // largest exponent (the high words order like the magnitudes)
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < kNormPiece; e++) {
+            const uint32_t hi = (uint32_t)(__builtin_bit_cast(uint64_t, n[e]) >> 32) & 0x7fffffffu;
+            top = hi > top ? hi : top;
+        }
+        top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+        if (!live) continue;
+        const bool bad = top >= 0x7ff00000u;  // a NaN or an infinity
+        int se = (int)(top >> 20) - 1023 - 8;  // a zero or subnormal block: below -127
+        se = se < -127 ? -127 : (se > 127 ? 127 : se);
+        uint32_t code[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            float q[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) q[e] = bad ? 0.f : (float)sticky(ldexp(n[4 * h + e], -se));
+            code[h] = e4m3_pack4(q);
+        }
+        *reinterpret_cast<uint2*>(a.codes + t * H + i * kNormPiece) = make_uint2(code[0], code[1]);
+        if ((i & 3) == 0) a.scales[t * (H / 32) + i / 4] = bad ? 255 : (uint8_t)(se + 127);
+    }
+}
+
+template <typename X, typename R>
+hipError_t launch_typed(const moe_rmsnorm_args& a, hipStream_t stream) {
+    const int pieces = (int)(a.hidden / kNormPiece);
+    const unsigned T = (unsigned)a.num_tokens;
+    if (pieces <= 64) rmsnorm_kernel<X, R, 1, 1><<<(T + 3) / 4, 256, 0, stream>>>(a);
+    else if (pieces <= 256) rmsnorm_kernel<X, R, 4, 1><<<T, 256, 0, stream>>>(a);
+    else if (pieces <= 512) rmsnorm_kernel<X, R, 4, 2><<<T, 256, 0, stream>>>(a);
+    else if (pieces <= 1024) rmsnorm_kernel<X, R, 4, 4><<<T, 256, 0, stream>>>(a);
+    else rmsnorm_kernel<X, R, 4, 8><<<T, 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const moe_rmsnorm_args& a, hipStream_t stream) {
+    const bool xb = a.x_dtype == MOE_DT_BF16, rb = !a.residual || a.residual_dtype == MOE_DT_BF16;
+    if (xb) return rb ? launch_typed<uint16_t, uint16_t>(a, stream) : launch_typed<uint16_t, float>(a, stream);
+    return rb ? launch_typed<float, uint16_t>(a, stream) : launch_typed<float, float>(a, stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,219 @@
+"""The operators around the layer without a GPU: what their header declares is
+exported and bound, and every refused call returns its status before any HIP
+call (nothing here dereferences a pointer)."""
+import ctypes
+import os
+import re
+
+import pytest
+
+from tests.conftest import ROOT, gpu_available
+
+HEADER = os.path.join(ROOT, "include", "ops", "moe_ops.h")
+
+
+@pytest.fixture(scope="module")
+def O():
+    from mxfp4_moe_expert_02_amd import _lib, _ops
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.fail("libmoe_mxfp4.so is not built (run __graft_entry__.build())")
+    _ops.ops_lib()
+    return _ops
+
+
+def test_declared_exported_and_bound(O):
+    import mxfp4_moe_expert_02_amd as M
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = set(re.findall(r"^\w+ (moe_\w+)\(", text, re.M))
+    assert names == set(O.OPS_EXPORTED)
+    for n in names:
+        assert hasattr(O.ops_lib(), n) and callable(getattr(M, n))
+    for struct in ("moe_rmsnorm_args", "moe_mxfp8_linear_args", "moe_dispatch_args", "moe_combine_args"):
+        body = re.search(r"typedef struct %s \{(.*?)\}" % struct, text, re.S).group(1)
+        fields = re.findall(r"(\w+);", body)
+        assert fields == [f for f, _ in getattr(O, struct)._fields_], struct
+    for name, value in re.findall(r"#define (MOE_EPI_\w+) (\d+)", text):
+        assert getattr(M, name) == int(value)
+
+
+def _norm(O, **over):
+    from mxfp4_moe_expert_02_amd import MOE_DT_BF16, MOE_DT_F32
+    a = dict(x=0x1000, x_dtype=MOE_DT_BF16, residual=0x2000, residual_dtype=MOE_DT_F32, residual_out=0x3000,
+             weight=0x4000, weight_dtype=MOE_DT_F32, eps=1e-5, y=0x5000, codes=0x6000, scales=0x7000, num_tokens=4,
+             hidden=256)
+    a.update(over)
+    return O.ops_lib().moe_rmsnorm(ctypes.byref(O.moe_rmsnorm_args(**a)), None)
+
+
+def test_rmsnorm_refusals(O):
+    from mxfp4_moe_expert_02_amd import (MOE_DT_BF16, MOE_DT_U8, MOE_E_ALIGN, MOE_E_DTYPE, MOE_E_HIP, MOE_E_NULL,
+                                         MOE_E_OPTION, MOE_E_SHAPE, MOE_OK)
+    assert O.ops_lib().moe_rmsnorm(None, None) == MOE_E_NULL
+    for kw in (dict(hidden=0), dict(hidden=31), dict(hidden=40), dict(hidden=16416), dict(num_tokens=-1),
+               dict(num_tokens=(1 << 22) + 1), dict(x_stride=255), dict(residual_stride=128), dict(y_stride=-256),
+               dict(residual_out=0x2000, residual_out_stride=512),
+               dict(residual_dtype=MOE_DT_BF16, residual_out=0x1000, residual_out_stride=512)):
+        assert _norm(O, **kw) == MOE_E_SHAPE, kw
+    for kw in (dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(reserved=1)):
+        assert _norm(O, **kw) == MOE_E_OPTION, kw
+    for kw in (dict(x_dtype=MOE_DT_U8), dict(residual_dtype=0), dict(weight_dtype=9), dict(residual_out=0x1000)):
+        assert _norm(O, **kw) == MOE_E_DTYPE, kw
+    for kw in (dict(x=0), dict(weight=0), dict(y=0, codes=0, scales=0), dict(codes=0), dict(scales=0),
+               dict(residual=0)):
+        assert _norm(O, **kw) == MOE_E_NULL, kw
+    for kw in (dict(x=0x1008), dict(weight=0x4004), dict(y=0x5002), dict(codes=0x6008), dict(scales=0x7002),
+               dict(x_stride=260), dict(residual_stride=258), dict(residual_out_stride=258), dict(y_stride=260)):
+        assert _norm(O, **kw) == MOE_E_ALIGN, kw
+    assert _norm(O, num_tokens=0, x=0) == MOE_OK
+    if not gpu_available():   # nothing to refuse: on to the launch, which finds no device
+        assert _norm(O) == MOE_E_HIP
+        assert _norm(O, y=0) == MOE_E_HIP and _norm(O, codes=0, scales=0) == MOE_E_HIP
+
+
+def _linear(O, **over):
+    a = dict(x_codes=0x1000, x_scales=0x2000, w_tiles=0x3000, w_scales=0x4000, out=0x5000, num_tokens=9, rows=128,
+             inner=256, workspace=0x10000, workspace_bytes=1 << 40)
+    a.update(over)
+    return O.ops_lib().moe_mxfp8_linear(ctypes.byref(O.moe_mxfp8_linear_args(**a)), None)
+
+
+def test_linear_refusals(O):
+    from mxfp4_moe_expert_02_amd import (MOE_E_ALIGN, MOE_E_HIP, MOE_E_LIMIT, MOE_E_NULL, MOE_E_OPTION, MOE_E_SHAPE,
+                                         MOE_OK)
+    assert O.ops_lib().moe_mxfp8_linear(None, None) == MOE_E_NULL
+    for kw in (dict(rows=0), dict(rows=96), dict(rows=(1 << 20) + 64), dict(inner=0), dict(inner=192),
+               dict(inner=65664), dict(num_tokens=-1), dict(num_tokens=(1 << 20) + 1), dict(out_stride=127),
+               dict(residual=0x6000, residual_stride=8), dict(residual=0x5000, residual_stride=256)):
+        assert _linear(O, **kw) == MOE_E_SHAPE, kw
+    for kw in (dict(activation=-1), dict(activation=4), dict(reserved=3), dict(out=0),
+               dict(out_codes=0x8000, out_scales=0x9000)):
+        assert _linear(O, **kw) == MOE_E_OPTION, kw
+    for kw in (dict(x_codes=0), dict(x_scales=0), dict(w_tiles=0), dict(w_scales=0), dict(out_codes=0x8000),
+               dict(out=0, out_scales=0x8000)):
+        assert _linear(O, **kw) == MOE_E_NULL, kw
+    for kw in (dict(x_codes=0x1008), dict(x_scales=0x2002), dict(w_tiles=0x3004), dict(w_scales=0x4008),
+               dict(out=0x5008), dict(bias=0x6004), dict(residual=0x6008), dict(out_stride=132),
+               dict(residual=0x6000, residual_stride=132), dict(workspace=0x10004),
+               dict(out=0, out_codes=0x8004, out_scales=0x9000)):
+        assert _linear(O, **kw) == MOE_E_ALIGN, kw
+    assert _linear(O, num_tokens=0, x_codes=0) == MOE_OK
+    L = O.ops_lib()
+    assert L.moe_mxfp8_linear_workspace(9, 96, 256, 0) == MOE_E_SHAPE
+    assert L.moe_mxfp8_linear_workspace(9, 128, 256, 7) == MOE_E_OPTION
+    for T in (1, 9, 40, 100, 288, 1001, 4096, 1 << 20):
+        for rows in (64, 448, 2048, 7168):
+            for K in (128, 2048, 7168, 65536):
+                need = L.moe_mxfp8_linear_workspace(T, rows, K, 0)
+                assert 0 <= need <= 4 * 8 * min(T, 1024) * rows + 4096, (T, rows, K)
+                if need:
+                    kw = dict(num_tokens=T, rows=rows, inner=K)
+                    assert _linear(O, workspace=0, **kw) == MOE_E_NULL
+                    assert _linear(O, workspace_bytes=need - 1, **kw) == MOE_E_LIMIT
+    if not gpu_available():
+        assert _linear(O) == MOE_E_HIP
+        assert _linear(O, out=0, out_codes=0x8000, out_scales=0x9000) == MOE_E_HIP
+
+
+def _dispatch(O, **over):
+    from mxfp4_moe_expert_02_amd import MOE_DT_BF16
+    a = dict(ids=0x1000, x=0x2000, offsets=0x3000, sorted=0x4000, pos=0x5000, rows=0x6000, num_tokens=9,
+             num_experts=8, hidden=100, top_k=2, dtype=MOE_DT_BF16)
+    a.update(over)
+    return O.ops_lib().moe_dispatch(ctypes.byref(O.moe_dispatch_args(**a)), None)
+
+
+def test_dispatch_refusals(O):
+    from mxfp4_moe_expert_02_amd import (MOE_DT_F32, MOE_DT_I32, MOE_DT_U8, MOE_E_ALIGN, MOE_E_DTYPE, MOE_E_HIP,
+                                         MOE_E_LIMIT, MOE_E_NULL, MOE_E_SHAPE, MOE_E_TOPK)
+    mx = dict(dtype=MOE_DT_U8, hidden=128, x_scales=0x7000, row_scales=0x8000)
+    assert O.ops_lib().moe_dispatch(None, None) == MOE_E_NULL
+    for kw in (dict(num_tokens=-1), dict(num_tokens=(1 << 24) + 1), dict(num_experts=0), dict(num_experts=1025),
+               dict(hidden=0), dict(hidden=65537), dict(mx, hidden=100), dict(x_stride=99)):
+        assert _dispatch(O, **kw) == MOE_E_SHAPE, kw
+    for kw in (dict(top_k=0), dict(top_k=33)):
+        assert _dispatch(O, **kw) == MOE_E_TOPK, kw
+    for kw in (dict(ids=0), dict(offsets=0), dict(pos=0), dict(x=0), dict(rows=0), dict(mx, x_scales=0),
+               dict(mx, row_scales=0), dict(x_scales=0x7000), dict(num_tokens=0, offsets=0)):
+        assert _dispatch(O, **kw) == MOE_E_NULL, kw
+    for kw in (dict(ids=0x1002), dict(offsets=0x3001), dict(sorted=0x4002), dict(pos=0x5002), dict(counts=0x9002),
+               dict(x=0x2001), dict(dtype=MOE_DT_F32, rows=0x6002)):
+        assert _dispatch(O, **kw) == MOE_E_ALIGN, kw
+    for dt in (0, MOE_DT_I32):
+        assert _dispatch(O, dtype=dt) == MOE_E_DTYPE
+    L = O.ops_lib()
+    assert L.moe_dispatch_workspace(10, 0, 2) == MOE_E_SHAPE and L.moe_dispatch_workspace(10, 4, 40) == MOE_E_TOPK
+    for T, E, k in ((100_000, 64, 8), (1 << 20, 1024, 32), (4096, 128, 8)):
+        need = L.moe_dispatch_workspace(T, E, k)
+        assert 0 < need <= 4 * 2049 * (E + 1) * 2 + 4096
+        kw = dict(num_tokens=T, num_experts=E, top_k=k)
+        assert _dispatch(O, **kw) == MOE_E_NULL
+        assert _dispatch(O, workspace=0xa000, workspace_bytes=need - 1, **kw) == MOE_E_LIMIT
+        assert _dispatch(O, workspace=0xa002, workspace_bytes=need, **kw) == MOE_E_ALIGN
+    if not gpu_available():
+        for kw in (dict(), mx, dict(x=0, rows=0), dict(sorted=0)):
+            assert _dispatch(O, **kw) == MOE_E_HIP, kw
+
+
+def _combine(O, fn="moe_combine", **over):
+    from mxfp4_moe_expert_02_amd import MOE_DT_BF16, MOE_DT_F32
+    a = dict(rows=0x1000, weights=0x2000, pos=0x3000, out=0x4000, dout=0x5000, drows=0x6000, dweights=0x7000,
+             num_tokens=9, num_rows=18, hidden=100, top_k=2, rows_dtype=MOE_DT_BF16, out_dtype=MOE_DT_F32)
+    a.update(over)
+    return getattr(O.ops_lib(), fn)(ctypes.byref(O.moe_combine_args(**a)), None)
+
+
+@pytest.mark.parametrize("fn", ["moe_combine", "moe_combine_backward", "moe_dispatch_backward"])
+def test_combine_refusals(O, fn):
+    from mxfp4_moe_expert_02_amd import (MOE_DT_U8, MOE_E_ALIGN, MOE_E_DTYPE, MOE_E_HIP, MOE_E_NULL, MOE_E_OPTION,
+                                         MOE_E_SHAPE, MOE_E_TOPK, MOE_OK)
+    base = dict(weights=0) if fn == "moe_dispatch_backward" else {}
+    call = lambda **kw: _combine(O, fn, **{**base, **kw})
+    back = fn == "moe_combine_backward"
+    assert getattr(O.ops_lib(), fn)(None, None) == MOE_E_NULL
+    for kw in (dict(num_tokens=-1), dict(num_tokens=(1 << 25) + 1), dict(num_tokens=1 << 25), dict(num_rows=-1),
+               dict(num_rows=(1 << 25) + 1), dict(hidden=0), dict(hidden=65537), dict(rows_stride=99),
+               dict(out_stride=1), dict(dout_stride=-5)):
+        assert call(**kw) == MOE_E_SHAPE, kw
+    for kw in (dict(top_k=0), dict(top_k=33)):
+        assert call(**kw) == MOE_E_TOPK, kw
+    for kw in (dict(rows_dtype=MOE_DT_U8), dict(out_dtype=0)):
+        assert call(**kw) == MOE_E_DTYPE, kw
+    assert call(reserved=1) == MOE_E_OPTION
+    nulls = [dict(pos=0), dict(rows=0)]
+    nulls += [dict(dout=0), dict(drows=0, dweights=0)] if back else [dict(out=0)]
+    for kw in nulls:
+        assert call(**kw) == MOE_E_NULL, kw
+    for kw in (dict(pos=0x3002), dict(rows=0x1001), dict(out=0x4002), dict(dout=0x5002), dict(dweights=0x7001)):
+        assert call(**kw) == MOE_E_ALIGN, kw
+    if back:
+        assert call(drows=0x1000, drows_stride=200) == MOE_E_SHAPE
+    if fn == "moe_dispatch_backward":
+        assert call(weights=0x2000) == MOE_E_OPTION
+    assert call(num_tokens=0, pos=0) == MOE_OK
+    if not gpu_available():
+        assert call() == MOE_E_HIP
+        assert call(rows=0, num_rows=0) == MOE_E_HIP
+        if back:
+            assert call(rows=0, dweights=0) == MOE_E_HIP
+
+
+def test_binding_refuses_other_memory(O):
+    """Host tensors, wrong types, shapes and strides raise before any call."""
+    import torch
+
+    import mxfp4_moe_expert_02_amd as M
+    b = torch.zeros(4, 64, dtype=torch.bfloat16)
+    i = torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="current device"):
+        M.moe_rmsnorm(b, torch.zeros(64), 1e-5, y=b)
+    with pytest.raises(ValueError, match="x: expected"):
+        M.moe_rmsnorm(b.half(), torch.zeros(64), 1e-5, y=b)
+    with pytest.raises(ValueError, match="current device"):
+        M.moe_combine(b, None, i, b)
+    with pytest.raises(ValueError, match="pos"):
+        M.moe_combine(b, None, i.long(), b)
+    with pytest.raises(ValueError, match="ids"):
+        M.moe_dispatch(b, i[0], 8, i, i, i, b)
+    u = torch.zeros(4, 128, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="x_codes"):
+        M.moe_mxfp8_linear(b, u, u, u, out=b)
