@@ -11,9 +11,12 @@ caller orders it against the tensors' own, as for any torch tensor.
 from __future__ import annotations
 
 import ctypes
+import struct
+
+import torch
 
 from . import _lib
-from ._lib import MOE_DT_BF16, MOE_DT_F32, MOE_DT_U8, _check, _ptr, _stream
+from ._lib import MOE_DT_BF16, MOE_DT_F32, MOE_DT_U8, _check
 
 MOE_EPI_NONE = 0
 MOE_EPI_SILU = 1
@@ -57,7 +60,26 @@ class moe_combine_args(ctypes.Structure):
                 ("reserved", _i32)]
 
 
+_FORMAT = {_vp: "Q", _i64: "q", _i32: "i", ctypes.c_double: "d"}
+
+
+def _packer(struct_type):
+    """The pack function of an argument structure: its fields in order, with
+    the compiler's own alignment.  A call hands the library the packed bytes
+    (building a ctypes structure field by field costs several microseconds,
+    as much as the smallest operators' GPU time)."""
+    s = struct.Struct("@" + "".join(_FORMAT[t] for _, t in struct_type._fields_))
+    assert s.size == ctypes.sizeof(struct_type)
+    return s.pack
+
+
+_pack_rmsnorm = _packer(moe_rmsnorm_args)
+_pack_linear = _packer(moe_mxfp8_linear_args)
+_pack_dispatch = _packer(moe_dispatch_args)
+_pack_combine = _packer(moe_combine_args)
+
 _ready = None
+_entry = {}
 
 
 def ops_lib() -> ctypes.CDLL:
@@ -65,12 +87,11 @@ def ops_lib() -> ctypes.CDLL:
     global _ready
     L = _lib.lib()
     if _ready is not L:
-        for name, args in (("moe_rmsnorm", moe_rmsnorm_args), ("moe_mxfp8_linear", moe_mxfp8_linear_args),
-                           ("moe_dispatch", moe_dispatch_args), ("moe_combine", moe_combine_args),
-                           ("moe_combine_backward", moe_combine_args),
-                           ("moe_dispatch_backward", moe_combine_args)):
-            fn = getattr(L, name)
-            fn.restype, fn.argtypes = ctypes.c_int, [ctypes.POINTER(args), _vp]
+        for name in OPS_EXPORTED:
+            if name.endswith("_workspace"):
+                continue
+            getattr(L, name).restype, getattr(L, name).argtypes = ctypes.c_int, [_vp, _vp]
+            _entry[name] = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, _vp)((name, L))
         L.moe_mxfp8_linear_workspace.restype = _i64
         L.moe_mxfp8_linear_workspace.argtypes = [_i64, _i64, _i64, _i32]
         L.moe_dispatch_workspace.restype = _i64
@@ -79,31 +100,55 @@ def ops_lib() -> ctypes.CDLL:
     return L
 
 
-def _want(t, name, dtypes, shape, strided=False):
-    """t is a tensor of the current device with one of the element types and
-    the shape, contiguous or (``strided``, two dimensions) with contiguous
-    rows.  Returns the distance between its rows in elements."""
-    import torch
-    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+# the current stream's handle without the Stream object around it (torch's own
+# generated code asks for it this way; 0.1 us against 3 us)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: _lib._stream(None))
+_device = torch.cuda.current_device
+
+
+def _call(name, packed, stream, check):
+    if _ready is None:
+        ops_lib()
+    rc = _entry[name](packed, _current_stream(_device()) if stream is None else _lib._stream(stream))
+    return _check(rc, name) if check and rc else rc
+
+
+def _want(t, name, dtypes, shape, dev, strided=False):
+    """t is a tensor of device `dev` with one of the element types and the
+    shape, contiguous or (``strided``, two dimensions) with contiguous rows.
+    Returns its address."""
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and (t.is_contiguous() or (
+            strided and (shape[1] <= 1 or t.stride(1) == 1) and t.stride(0) >= shape[1])):
+        return t.data_ptr()
+    if t.dtype not in dtypes or t.shape != shape:
         raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor of the current device, got {t.device}")
-    if t.is_contiguous():
-        return t.shape[-1] if t.dim() == 2 else 0
-    if not strided or (t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: expected contiguous {'rows' if strided else 'memory'}, got strides {t.stride()}")
-    return t.stride(0)
+    raise ValueError(f"{name}: expected contiguous {'rows' if strided else 'memory'}, got strides {t.stride()}")
 
 
-def _dt(t):
-    import torch
-    return {torch.bfloat16: MOE_DT_BF16, torch.float32: MOE_DT_F32, torch.uint8: MOE_DT_U8}[t.dtype]
+def _row(t):
+    """The distance between t's rows (any, where it has one row at most)."""
+    return t.stride(0) if t.shape[0] > 1 else 0
 
 
-def _floats():
-    import torch
-    return (torch.bfloat16, torch.float32)
+_BF16, _F32, _U8, _I32 = (torch.bfloat16,), (torch.float32,), (torch.uint8,), (torch.int32,)
+_FLOATS = _BF16 + _F32
+_ROWS = _FLOATS + _U8
+_DT = {torch.bfloat16: MOE_DT_BF16, torch.float32: MOE_DT_F32, torch.uint8: MOE_DT_U8}
+
+
+def _dev(t):
+    """The current device, if t is a device tensor (no context is made for a
+    host tensor, which then fails its check)."""
+    return _device() if t.is_cuda else 0
+
+
+def _matrix(t, name, what):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected {what}, got {tuple(t.shape)}")
+    return t.shape
 
 
 def moe_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None, codes=None, scales=None,
@@ -115,33 +160,22 @@ def moe_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None,
     type; may be ``residual`` itself), y [T, H] bfloat16, and codes [T, H] with
     scales [T, H/32] uint8 (MXFP8).  Rows of x, residual, residual_out and y
     may be strided."""
-    import torch
-    if x.dim() != 2:
-        raise ValueError(f"x: expected [tokens, hidden], got {tuple(x.shape)}")
-    T, H = x.shape
-    a = moe_rmsnorm_args(num_tokens=T, hidden=H, eps=eps, x=_ptr(x), weight=_ptr(weight))
-    a.x_stride = _want(x, "x", _floats(), (T, H), strided=True)
-    a.x_dtype = _dt(x)
-    _want(weight, "weight", _floats(), (H,))
-    a.weight_dtype = _dt(weight)
+    shape = T, H = _matrix(x, "x", "[tokens, hidden]")
+    dev = _dev(x)
+    px, pw = _want(x, "x", _FLOATS, shape, dev, True), _want(weight, "weight", _FLOATS, (H,), dev)
+    pr = ld_r = po = ld_o = py = ld_y = dt_r = 0
     if residual is not None:
-        a.residual, a.residual_stride = _ptr(residual), _want(residual, "residual", _floats(), (T, H), strided=True)
-        a.residual_dtype = _dt(residual)
+        pr, ld_r, dt_r = _want(residual, "residual", _FLOATS, shape, dev, True), _row(residual), _DT[residual.dtype]
     if residual_out is not None:
         if residual is None:
             raise ValueError("residual_out: given without residual")
-        a.residual_out = _ptr(residual_out)
-        a.residual_out_stride = _want(residual_out, "residual_out", (residual.dtype,), (T, H), strided=True)
+        po, ld_o = _want(residual_out, "residual_out", (residual.dtype,), shape, dev, True), _row(residual_out)
     if y is not None:
-        a.y, a.y_stride = _ptr(y), _want(y, "y", (torch.bfloat16,), (T, H), strided=True)
-    if codes is not None:
-        _want(codes, "codes", (torch.uint8,), (T, H))
-        a.codes = _ptr(codes)
-    if scales is not None:
-        _want(scales, "scales", (torch.uint8,), (T, H // 32))
-        a.scales = _ptr(scales)
-    rc = ops_lib().moe_rmsnorm(ctypes.byref(a), _stream(stream))
-    return _check(rc, "moe_rmsnorm") if check else rc
+        py, ld_y = _want(y, "y", _BF16, shape, dev, True), _row(y)
+    pc = 0 if codes is None else _want(codes, "codes", _U8, shape, dev)
+    ps = 0 if scales is None else _want(scales, "scales", _U8, (T, H // 32), dev)
+    return _call("moe_rmsnorm", _pack_rmsnorm(px, _row(x), _DT[x.dtype], dt_r, pr, ld_r, po, ld_o, pw,
+                                              _DT[weight.dtype], 0, eps, py, ld_y, pc, ps, T, H), stream, check)
 
 
 def moe_mxfp8_linear_workspace(num_tokens: int, rows: int, inner: int, activation: int = MOE_EPI_NONE) -> int:
@@ -162,39 +196,25 @@ def moe_mxfp8_linear(x_codes, x_scales, w_tiles, w_scales, out=None, out_codes=N
     out_codes [T, cols] and out_scales [T, cols/32] uint8, where cols is rows,
     or rows / 2 for MOE_EPI_SILU_MUL.  workspace: a uint8 tensor of at least
     moe_mxfp8_linear_workspace(...) bytes, or None if that is 0."""
-    import torch
-    u8 = (torch.uint8,)
-    if x_codes.dim() != 2 or w_tiles.dim() != 2:
-        raise ValueError(f"expected x_codes [tokens, inner] and w_tiles [rows, inner], got {tuple(x_codes.shape)} "
-                         f"and {tuple(w_tiles.shape)}")
-    T, K = x_codes.shape
-    rows = w_tiles.shape[0]
+    T, K = _matrix(x_codes, "x_codes", "[tokens, inner]")
+    rows = _matrix(w_tiles, "w_tiles", "[rows, inner]")[0]
     cols = rows // 2 if activation == MOE_EPI_SILU_MUL else rows
-    _want(x_codes, "x_codes", u8, (T, K))
-    _want(x_scales, "x_scales", u8, (T, K // 32))
-    _want(w_tiles, "w_tiles", u8, (rows, K))
-    _want(w_scales, "w_scales", u8, (rows, K // 32))
-    a = moe_mxfp8_linear_args(x_codes=_ptr(x_codes), x_scales=_ptr(x_scales), w_tiles=_ptr(w_tiles),
-                              w_scales=_ptr(w_scales), num_tokens=T, rows=rows, inner=K, activation=activation)
-    if bias is not None:
-        _want(bias, "bias", (torch.float32,), (rows,))
-        a.bias = _ptr(bias)
+    dev = _dev(x_codes)
+    px, pxs = _want(x_codes, "x_codes", _U8, (T, K), dev), _want(x_scales, "x_scales", _U8, (T, K // 32), dev)
+    pw, pws = _want(w_tiles, "w_tiles", _U8, (rows, K), dev), _want(w_scales, "w_scales", _U8, (rows, K // 32), dev)
+    pr = ld_r = po = ld_o = nw = 0
+    pb = 0 if bias is None else _want(bias, "bias", _F32, (rows,), dev)
     if residual is not None:
-        a.residual = _ptr(residual)
-        a.residual_stride = _want(residual, "residual", (torch.bfloat16,), (T, cols), strided=True)
+        pr, ld_r = _want(residual, "residual", _BF16, (T, cols), dev, True), _row(residual)
     if out is not None:
-        a.out, a.out_stride = _ptr(out), _want(out, "out", (torch.bfloat16,), (T, cols), strided=True)
-    if out_codes is not None:
-        _want(out_codes, "out_codes", u8, (T, cols))
-        a.out_codes = _ptr(out_codes)
-    if out_scales is not None:
-        _want(out_scales, "out_scales", u8, (T, cols // 32))
-        a.out_scales = _ptr(out_scales)
+        po, ld_o = _want(out, "out", _BF16, (T, cols), dev, True), _row(out)
+    pc = 0 if out_codes is None else _want(out_codes, "out_codes", _U8, (T, cols), dev)
+    ps = 0 if out_scales is None else _want(out_scales, "out_scales", _U8, (T, cols // 32), dev)
+    pk = 0
     if workspace is not None:
-        _want(workspace, "workspace", u8, workspace.shape)
-        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
-    rc = ops_lib().moe_mxfp8_linear(ctypes.byref(a), _stream(stream))
-    return _check(rc, "moe_mxfp8_linear") if check else rc
+        pk, nw = _want(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel()
+    return _call("moe_mxfp8_linear", _pack_linear(px, pxs, pw, pws, pb, pr, ld_r, po, ld_o, pc, ps, pk, nw, T, rows,
+                                                  K, activation, 0), stream, check)
 
 
 def moe_dispatch_workspace(num_tokens: int, num_experts: int, top_k: int) -> int:
@@ -214,67 +234,41 @@ def moe_dispatch(x, ids, num_experts: int, offsets, sorted, pos, rows, workspace
     whose id is outside 0 .. num_experts-1 gets pos -1 and no row; sorted and
     rows behind offsets[E] are left as they were.  workspace: a uint8 tensor
     of at least moe_dispatch_workspace(...) bytes, or None if that is 0."""
-    import torch
-    i32, u8 = (torch.int32,), (torch.uint8,)
-    if ids.dim() != 2:
-        raise ValueError(f"ids: expected [tokens, top_k], got {tuple(ids.shape)}")
-    T, k = ids.shape
-    _want(ids, "ids", i32, (T, k))
-    _want(offsets, "offsets", i32, (num_experts + 1,))
-    _want(pos, "pos", i32, (T, k))
-    a = moe_dispatch_args(ids=_ptr(ids), offsets=_ptr(offsets), pos=_ptr(pos), num_tokens=T,
-                          num_experts=num_experts, top_k=k)
-    if sorted is not None:
-        _want(sorted, "sorted", i32, (T * k,))
-        a.sorted = _ptr(sorted)
-    if counts is not None:
-        _want(counts, "counts", i32, (num_experts,))
-        a.counts = _ptr(counts)
+    T, k = _matrix(ids, "ids", "[tokens, top_k]")
+    dev = _dev(ids)
+    pi = _want(ids, "ids", _I32, (T, k), dev)
+    pf = _want(offsets, "offsets", _I32, (num_experts + 1,), dev)
+    pp = _want(pos, "pos", _I32, (T, k), dev)
+    pt = 0 if sorted is None else _want(sorted, "sorted", _I32, (T * k,), dev)
+    pn = 0 if counts is None else _want(counts, "counts", _I32, (num_experts,), dev)
+    px = ld_x = pxs = pr = prs = pk = nw = H = dt = 0
     if (x is None) != (rows is None):
         raise ValueError("x and rows: both or neither")
     if x is not None:
-        if x.dim() != 2:
-            raise ValueError(f"x: expected [tokens, hidden], got {tuple(x.shape)}")
-        H = x.shape[1]
-        mx = x.dtype == torch.uint8
-        a.hidden, a.x, a.rows = H, _ptr(x), _ptr(rows)
-        a.x_stride = _want(x, "x", (*_floats(), torch.uint8), (T, H), strided=True)
-        a.dtype = _dt(x)
-        _want(rows, "rows", (x.dtype,), (T * k, H))
+        H = _matrix(x, "x", "[tokens, hidden]")[1]
+        px, ld_x, dt = _want(x, "x", _ROWS, (T, H), dev, True), _row(x), _DT[x.dtype]
+        pr = _want(rows, "rows", (x.dtype,), (T * k, H), dev)
+        mx = dt == MOE_DT_U8
         if mx != (x_scales is not None) or mx != (row_scales is not None):
             raise ValueError("x_scales and row_scales: with uint8 rows (MXFP8), and only with them")
         if mx:
-            _want(x_scales, "x_scales", u8, (T, H // 32))
-            _want(row_scales, "row_scales", u8, (T * k, H // 32))
-            a.x_scales, a.row_scales = _ptr(x_scales), _ptr(row_scales)
+            pxs = _want(x_scales, "x_scales", _U8, (T, H // 32), dev)
+            prs = _want(row_scales, "row_scales", _U8, (T * k, H // 32), dev)
     if workspace is not None:
-        _want(workspace, "workspace", u8, workspace.shape)
-        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
-    rc = ops_lib().moe_dispatch(ctypes.byref(a), _stream(stream))
-    return _check(rc, "moe_dispatch") if check else rc
-
-
-def _slots(pos, weights, top):
-    import torch
-    if pos.dim() != 2:
-        raise ValueError(f"pos: expected [tokens, top_k], got {tuple(pos.shape)}")
-    _want(pos, "pos", (torch.int32,), pos.shape)
-    if weights is not None:
-        _want(weights, "weights", (torch.float32,), pos.shape)
-    if top.dim() != 2 or top.shape[0] != pos.shape[0]:
-        raise ValueError(f"expected [{pos.shape[0]}, hidden] token rows, got {tuple(top.shape)}")
-    return moe_combine_args(pos=_ptr(pos), weights=_ptr(weights), num_tokens=pos.shape[0], top_k=pos.shape[1],
-                            hidden=top.shape[1], out_dtype=_dt(top) if top.dtype in _floats() else 0)
+        pk, nw = _want(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel()
+    return _call("moe_dispatch", _pack_dispatch(pi, px, ld_x, pxs, pn, pf, pt, pp, pr, prs, pk, nw, T, num_experts, H,
+                                                k, dt), stream, check)
 
 
 def _combine(name, rows, weights, pos, out, stream, check):
-    a = _slots(pos, weights, out)
-    n = rows.shape[0]
-    a.rows_stride = _want(rows, "rows", _floats(), (n, out.shape[1]), strided=True)
-    a.rows, a.num_rows, a.rows_dtype = _ptr(rows), n, _dt(rows)
-    a.out, a.out_stride = _ptr(out), _want(out, "out", _floats(), tuple(out.shape), strided=True)
-    rc = getattr(ops_lib(), name)(ctypes.byref(a), _stream(stream))
-    return _check(rc, name) if check else rc
+    slots = T, k = _matrix(pos, "pos", "[tokens, top_k]")
+    shape = _matrix(out, "out", "[tokens, hidden]")
+    H, n, dev = shape[1], _matrix(rows, "rows", "[rows, hidden]")[0], _dev(pos)
+    pp = _want(pos, "pos", _I32, slots, dev)
+    pw = 0 if weights is None else _want(weights, "weights", _F32, slots, dev)
+    pr, po = _want(rows, "rows", _FLOATS, (n, H), dev, True), _want(out, "out", _FLOATS, (T, H), dev, True)
+    return _call(name, _pack_combine(pr, _row(rows), pw, pp, po, _row(out), 0, 0, 0, 0, 0, T, n, H, k,
+                                     _DT[rows.dtype], _DT[out.dtype], 0), stream, check)
 
 
 def moe_combine(rows, weights, pos, out, stream=None, check: bool = True) -> int:
@@ -295,16 +289,15 @@ def moe_combine_backward(dout, rows, weights, pos, drows=None, dweights=None, st
     (rows without a slot are left as they were) and dweights[t, j] =
     <dout[t], rows[pos[t, j]]>.  Either may be None; rows [R, H] gives the
     rows' type and is read for dweights only.  ``drows`` may be ``rows``."""
-    import torch
-    a = _slots(pos, weights, dout)
-    n, H = rows.shape[0], dout.shape[1]
-    a.rows_stride = _want(rows, "rows", _floats(), (n, H), strided=True)
-    a.rows, a.num_rows, a.rows_dtype = _ptr(rows), n, _dt(rows)
-    a.dout, a.dout_stride = _ptr(dout), _want(dout, "dout", _floats(), tuple(dout.shape), strided=True)
+    slots = T, k = _matrix(pos, "pos", "[tokens, top_k]")
+    H, n, dev = _matrix(dout, "dout", "[tokens, hidden]")[1], _matrix(rows, "rows", "[rows, hidden]")[0], _dev(pos)
+    pp = _want(pos, "pos", _I32, slots, dev)
+    pw = 0 if weights is None else _want(weights, "weights", _F32, slots, dev)
+    pr, pg = _want(rows, "rows", _FLOATS, (n, H), dev, True), _want(dout, "dout", _FLOATS, (T, H), dev, True)
+    pd = ld_d = 0
     if drows is not None:
-        a.drows, a.drows_stride = _ptr(drows), _want(drows, "drows", (rows.dtype,), (n, H), strided=True)
-    if dweights is not None:
-        _want(dweights, "dweights", (torch.float32,), pos.shape)
-        a.dweights = _ptr(dweights)
-    rc = ops_lib().moe_combine_backward(ctypes.byref(a), _stream(stream))
-    return _check(rc, "moe_combine_backward") if check else rc
+        pd, ld_d = _want(drows, "drows", (rows.dtype,), (n, H), dev, True), _row(drows)
+    pdw = 0 if dweights is None else _want(dweights, "dweights", _F32, slots, dev)
+    return _call("moe_combine_backward",
+                 _pack_combine(pr, _row(rows), pw, pp, 0, 0, pg, _row(dout), pd, ld_d, pdw, T, n, H, k,
+                               _DT[rows.dtype], _DT[dout.dtype], 0), stream, check)
