@@ -34,6 +34,7 @@
 // are free of bank conflicts); each wave then reads its A and B operands of
 // the chunk from LDS.  The token rows of x are gathered through the routing
 // order; h rows are already in that order.
+#include "lds_dma.h"
 #include "mfma_items.h"
 #include "mx_encode.h"
 
@@ -102,40 +103,6 @@ struct PfSmem {
 };
 
 __device__ inline int b_slot(int row, int piece) { return piece ^ ((row >> 1) & 7); }
-
-// Direct global -> LDS loads (16 or 4 bytes per lane; lane l's bytes land
-// at lds + 16 l, or 4 l).  Written as inline asm so that the compiler does
-// not treat every later LDS read as depending on them (it would wait for all
-// of them, a full drain, before each read); the main loop waits for them
-// itself.  M0 (the LDS base) is saved and restored inside the block.
-typedef __attribute__((address_space(3))) const void lds_cvoid_t;
-__device__ inline uint32_t lds_addr(const void* p) {
-    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_cvoid_t*)p);
-}
-__device__ inline void dma16(const uint8_t* src, uint32_t lds) {
-    uint32_t save;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %2\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %1, off\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(save)
-        : "v"(src), "s"(lds)
-        : "memory");
-}
-__device__ inline void dma4(const uint8_t* src, uint32_t lds) {
-    uint32_t save;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %2\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dword %1, off\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(save)
-        : "v"(src), "s"(lds)
-        : "memory");
-}
 
 // Two workgroup shapes share the loop below.  The routed experts (F8 =
 // false): two quads of MXFP4 weights (4 KB per quad and chunk), waves (wr,

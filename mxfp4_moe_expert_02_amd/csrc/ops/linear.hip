@@ -13,6 +13,7 @@
 // bits below about 2^-16 of the largest product of a group (measured: 1.4e-5
 // of the sum's rms against 4e-8), and at these sizes their rate is not
 // needed.
+#include "../lds_dma.h"
 #include "ops_internal.h"
 
 namespace moe {
@@ -264,44 +265,167 @@ __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear
     }
 }
 
-// One wave: one quad x 16 tokens over the whole inner axis, both operands
-// straight from global memory.
-__global__ void __launch_bounds__(kWave) linear_wave_kernel(moe_mxfp8_linear_args a) {
-    const int lane = threadIdx.x, c = lane % 16, g = lane / 16;
-    const int64_t quads = a.rows / 64, quad = blockIdx.x % quads, tile = blockIdx.x / quads;
-    const int chunks = (int)(a.inner / 128);
-    const int64_t t = 16 * tile + c;
-    const bool live = t < a.num_tokens;
-    const int64_t tt = live ? t : a.num_tokens - 1;
-    const uint8_t* x = a.x_codes + tt * a.inner + 16 * g;
-    const uint8_t* xs = a.x_scales + tt * (a.inner / 32) + g;
-    const uint8_t* w = a.w_tiles + quad * chunks * 8192 + (g & 1) * 1024 + (c + 16 * (g >> 1)) * 16;
-    const uint8_t* ws = a.w_scales + quad * chunks * 256 + lane * 4;
-    f32x4_t acc[4];
+// ----------------------------------------------------------- many tokens
+// A workgroup computes RQ quads x TT 16-token tiles; its WR x WT waves own
+// RQ / WR quads x TT / WT tiles each.  Per 128-k chunk both operands go from
+// global memory straight to LDS, in operand order: A as the tile layout has
+// it, B as [tile][piece][token][16 bytes], so that every operand read is a
+// contiguous 1 KB per wave, free of bank conflicts.  On the FP8 matrix cores
+// (v_mfma_scale_f32_16x16x128_f8f6f4): lane (r, g) of an operand holds the
+// 16-byte pieces g and g + 4 of row r's 128 bytes and the scale of block g.
+template <int RQ, int TT, int STAGES>
+struct TileSmem {
+    alignas(16) uint8_t a[STAGES][RQ][8192];
+    alignas(16) uint8_t b[STAGES][TT][2048];
+    alignas(16) uint32_t as[STAGES][RQ][kWave];
+    alignas(16) uint32_t bs[STAGES][TT * 16];
+};
+
+struct TileGrid {
+    int row_blocks, tok_blocks;
+    int splits, split_chunks;
+};
+
+template <int RQ, int TT, int WR, int WT>
+__global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_linear_args a, TileGrid p) {
+    constexpr int kStages = 2, kWaves = WR * WT;
+    constexpr int Q = RQ / WR, NT = TT / WT;              // a wave's quads and token tiles
+    constexpr int kA = RQ * 8 / kWaves, kB = TT * 2 / kWaves;  // 1 KB loads per wave and chunk
+    static_assert(RQ * 8 % kWaves == 0 && TT * 2 % kWaves == 0 && RQ + TT / 4 == kWaves, "loads per wave");
+    extern __shared__ uint8_t smem_raw[];
+    auto& sm = *reinterpret_cast<TileSmem<RQ, TT, kStages>*>(smem_raw);
+    const int w = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
+    const int per_split = p.row_blocks * p.tok_blocks;
+    const int split = blockIdx.x / per_split, blk = blockIdx.x % per_split;
+    const int rb = blk % p.row_blocks, tb = blk / p.row_blocks;
+    const int chunks = (int)(a.inner / 128), quads = (int)(a.rows / 64);
+    const int k0 = split * p.split_chunks, k1 = min(chunks, k0 + p.split_chunks);
+    const int q0 = rb * RQ;
+    const int64_t t0 = (int64_t)tb * (16 * TT);
+    const int last = (int)min((int64_t)(16 * TT), a.num_tokens - t0) - 1;  // rows past it repeat it
+
+    // this wave's loads of chunk k0 (quads past the end repeat the last one)
+    const uint8_t* srcA[kA];
+    const uint8_t* srcB[kB];
+    const uint8_t* srcS;
+    int step_s;
 #pragma unroll
-    for (int rg = 0; rg < 4; rg++) acc[rg] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int ch = 0; ch < chunks; ch++) {
-        const i32x8_t B = operand(*reinterpret_cast<const uint4*>(x + ch * 128),
-                                  *reinterpret_cast<const uint4*>(x + ch * 128 + 64));
-        const uint32_t sb = xs[ch * 4];
-        const uint32_t sa = *reinterpret_cast<const uint32_t*>(ws + (int64_t)ch * 256);
-        const uint8_t* wc = w + (int64_t)ch * 8192;
-        static_for<4>([&](auto rg) {
-            const i32x8_t A = operand(*reinterpret_cast<const uint4*>(wc + rg * 2048),
-                                      *reinterpret_cast<const uint4*>(wc + rg * 2048 + 512));
-            acc[rg] = mfma_scaled<0, rg, 0>(A, B, acc[rg], sa, sb);
-        });
+    for (int i = 0; i < kA; i++) {
+        const int piece = w * kA + i;  // quad piece / 8, 1 KB piece % 8
+        srcA[i] = a.w_tiles + ((int64_t)min(q0 + piece / 8, quads - 1) * chunks + k0) * 8192 + piece % 8 * 1024 + lane * 16;
     }
-    finish<4>(a, quad, 0, t, live, acc);
+#pragma unroll
+    for (int i = 0; i < kB; i++) {
+        const int piece = w * kB + i;  // tile piece / 2, pieces 4 (piece % 2) .. +3 of 16 tokens
+        const int64_t tok = t0 + min(piece / 2 * 16 + c, last);
+        srcB[i] = a.x_codes + tok * a.inner + (int64_t)k0 * 128 + (piece % 2) * 64 + g * 16;
+    }
+    if (w < RQ) {
+        srcS = a.w_scales + ((int64_t)min(q0 + w, quads - 1) * chunks + k0) * 256 + lane * 4;
+        step_s = 256;
+    } else {
+        const int64_t tok = t0 + min((w - RQ) * kWave + lane, last);
+        srcS = a.x_scales + tok * (a.inner / 32) + (int64_t)k0 * 4;
+        step_s = 4;
+    }
+    auto issue = [&](int k, int buf) {
+        const int d = k - k0;
+#pragma unroll
+        for (int i = 0; i < kA; i++)
+            dma16(srcA[i] + (int64_t)d * 8192, lds_addr(&sm.a[buf][0][(w * kA + i) * 1024]));
+#pragma unroll
+        for (int i = 0; i < kB; i++)
+            dma16(srcB[i] + d * 128, lds_addr(&sm.b[buf][0][(w * kB + i) * 1024]));
+        dma4(srcS + (int64_t)d * step_s, lds_addr(w < RQ ? (const void*)&sm.as[buf][w][0]
+                                                        : (const void*)&sm.bs[buf][(w - RQ) * kWave]));
+    };
+    const int wr = w % WR, wt = w / WR;
+    f32x4_t acc[Q][4][NT];
+#pragma unroll
+    for (int q = 0; q < Q; q++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int t = 0; t < NT; t++) acc[q][i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    issue(k0, 0);
+    int buf = 0;
+    const int a_lo = (g & 1) * 1024 + (c + 16 * (g >> 1)) * 16;  // piece g; piece g + 4 is 512 bytes on
+    for (int k = k0; k < k1; k++) {
+        // this wave's loads of chunk k have landed; after the barrier every
+        // wave's have, and every wave is done reading the other buffer
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        if (k + 1 < k1) issue(k + 1, buf ^ 1);
+        i32x8_t B[NT];
+        uint32_t sb[NT];
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+            const int tile = wt * NT + t;
+            B[t] = operand(*reinterpret_cast<const uint4*>(&sm.b[buf][tile][lane * 16]),
+                           *reinterpret_cast<const uint4*>(&sm.b[buf][tile][1024 + lane * 16]));
+            sb[t] = reinterpret_cast<const uint8_t*>(&sm.bs[buf][tile * 16 + c])[g];
+        }
+#pragma unroll
+        for (int q = 0; q < Q; q++) {
+            const uint8_t* qa = &sm.a[buf][wr * Q + q][a_lo];
+            const uint32_t sa = sm.as[buf][wr * Q + q][lane];
+            static_for<4>([&](auto i) {
+                const i32x8_t A = operand(*reinterpret_cast<const uint4*>(qa + i * 2048),
+                                          *reinterpret_cast<const uint4*>(qa + i * 2048 + 512));
+#pragma unroll
+                for (int t = 0; t < NT; t++) acc[q][i][t] = mfma_scaled<0, i, 0>(A, B[t], acc[q][i][t], sa, sb[t]);
+            });
+        }
+        buf ^= 1;
+    }
+    // The sums leave through this wave's own part of the LDS (one quad x tile
+    // a time, in the lanes' own order), so that the epilogue is one piece of
+    // code in a loop instead of Q * NT copies of it.
+    __syncthreads();
+    constexpr int kUnits = Q * NT;
+    constexpr int kRound = sizeof(TileSmem<RQ, TT, kStages>) / (kWaves * 4096) < kUnits
+                               ? sizeof(TileSmem<RQ, TT, kStages>) / (kWaves * 4096) : kUnits;
+    f32x4_t(*mine)[4][kWave] = reinterpret_cast<f32x4_t(*)[4][kWave]>(smem_raw + w * kRound * 4096);
+    static_for<(kUnits + kRound - 1) / kRound>([&](auto round) {
+        static_for<kRound>([&](auto u) {
+            constexpr int n = decltype(round)::value * kRound + decltype(u)::value;
+            if constexpr (n < kUnits) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) mine[u][i][lane] = acc[n / NT][i][n % NT];
+            }
+        });
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int u = 0; u < kRound; u++) {
+            const int n = round * kRound + u;
+            const int quad = q0 + wr * Q + n / NT;
+            const int64_t tile = (int64_t)tb * TT + wt * NT + n % NT;
+            if (n >= kUnits || quad >= quads || 16 * tile >= a.num_tokens) continue;
+            f32x4_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[i] = mine[u][i][lane];
+            if (p.splits > 1) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    *partial_of(a, split, tile, 4 * quad + i) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+            } else {
+                const int64_t t = 16 * tile + c;
+                finish<4>(a, quad, 0, t, t < a.num_tokens, v);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    });
 }
 
 // ------------------------------------------------------------ the choice
-constexpr int kRowsMaxTok = 128;  // tokens of linear_rows_kernel
+constexpr int kRowsMaxTok = 128;   // tokens of linear_rows_kernel
+constexpr int kSplitMaxTok = 1024;  // most tokens whose inner axis is split
 
 struct LinearPlan {
     bool rows;       // linear_rows_kernel
     int G, NT, W;
     RowsGrid grid;
+    bool wide;       // 256 x 256 tiles (else 128 x 128)
+    TileGrid tile;
 };
 
 LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation, bool mx) {
@@ -309,7 +433,23 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
     const int tiles = (int)((T + 15) / 16), chunks = (int)(inner / 128);
     const bool gated = activation == MOE_EPI_SILU_MUL;
     p.rows = T <= kRowsMaxTok;
-    if (!p.rows) return p;
+    if (!p.rows) {
+        const int64_t wide_blocks = (rows + 255) / 256 * ((T + 255) / 256);
+        p.wide = wide_blocks >= 192;
+        const int n = p.wide ? 256 : 128;
+        p.tile.row_blocks = (int)((rows + n - 1) / n);
+        p.tile.tok_blocks = (int)((T + n - 1) / n);
+        int64_t splits = 1;
+        if (!p.wide && T <= kSplitMaxTok) {
+            splits = 512 / ((int64_t)p.tile.row_blocks * p.tile.tok_blocks);
+            if (splits > chunks / 8) splits = chunks / 8;
+            if (splits > 8 * T / (16 * tiles)) splits = 8 * T / (16 * tiles);
+        }
+        p.tile.splits = splits < 1 ? 1 : (int)splits;
+        p.tile.split_chunks = (chunks + p.tile.splits - 1) / p.tile.splits;
+        p.tile.splits = (chunks + p.tile.split_chunks - 1) / p.tile.split_chunks;
+        return p;
+    }
     if (tiles <= 2) {
         p.G = mx ? (gated ? 4 : 2) : gated ? 2 : 1;
         p.NT = tiles;
@@ -340,34 +480,50 @@ void launch_rows(const moe_mxfp8_linear_args& a, const RowsGrid& p, hipStream_t 
     linear_rows_kernel<G, NT, W><<<grid, W * kWave, 0, stream>>>(a, p);
 }
 
+template <int RQ, int TT, int WR, int WT>
+hipError_t launch_tile(const moe_mxfp8_linear_args& a, const TileGrid& p, hipStream_t stream) {
+    constexpr int bytes = sizeof(TileSmem<RQ, TT, 2>);
+    const auto kernel = linear_tile_kernel<RQ, TT, WR, WT>;
+    if (bytes > 65536) {  // more than 64 KB of LDS has to be asked for
+        const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                   hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (err != hipSuccess) return err;
+    }
+    const unsigned grid = (unsigned)((int64_t)p.splits * p.row_blocks * p.tok_blocks);
+    kernel<<<grid, WR * WT * kWave, bytes, stream>>>(a, p);
+    return hipGetLastError();
+}
+
+int splits_of(const LinearPlan& p) { return p.rows ? p.grid.splits : p.tile.splits; }
+
 }  // namespace
 
 int64_t mxfp8_linear_workspace(int64_t T, int64_t rows, int64_t inner, int32_t activation) {
     if (T == 0) return 0;
-    const LinearPlan p = make_plan(T, rows, inner, activation, false);
-    return p.rows && p.grid.splits > 1 ? p.grid.splits * ((T + 15) / 16) * rows * 64 : 0;
+    const int splits = splits_of(make_plan(T, rows, inner, activation, false));
+    return splits > 1 ? splits * ((T + 15) / 16) * rows * 64 : 0;
 }
 
 hipError_t launch_mxfp8_linear(const moe_mxfp8_linear_args& a, hipStream_t stream) {
     const LinearPlan p = make_plan(a.num_tokens, a.rows, a.inner, a.activation, a.out_codes != nullptr);
-    if (!p.rows) {
-        const int64_t grid = a.rows / 64 * ((a.num_tokens + 15) / 16);
-        linear_wave_kernel<<<(unsigned)grid, kWave, 0, stream>>>(a);
-        return hipGetLastError();
-    }
     const RowsGrid& r = p.grid;
-    if (p.W == 8) {
+    hipError_t err = hipSuccess;
+    if (!p.rows) {
+        err = p.wide ? launch_tile<4, 16, 2, 4>(a, p.tile, stream) : launch_tile<2, 8, 2, 2>(a, p.tile, stream);
+    } else if (p.W == 8) {
         if (p.G == 1) p.NT == 1 ? launch_rows<1, 1, 8>(a, r, stream) : launch_rows<1, 2, 8>(a, r, stream);
         else if (p.G == 2) p.NT == 1 ? launch_rows<2, 1, 8>(a, r, stream) : launch_rows<2, 2, 8>(a, r, stream);
         else p.NT == 1 ? launch_rows<4, 1, 8>(a, r, stream) : launch_rows<4, 2, 8>(a, r, stream);
+        err = hipGetLastError();
     } else {
         if (p.NT <= 3) launch_rows<4, 3, 4>(a, r, stream);
         else launch_rows<4, 4, 4>(a, r, stream);
+        err = hipGetLastError();
     }
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess || r.splits == 1) return err;
+    const int splits = splits_of(p);
+    if (err != hipSuccess || splits == 1) return err;
     const int64_t units = a.rows / 64 * ((a.num_tokens + 15) / 16);
-    linear_finish_kernel<<<(unsigned)((units + 3) / 4), 256, 0, stream>>>(a, r.splits);
+    linear_finish_kernel<<<(unsigned)((units + 3) / 4), 256, 0, stream>>>(a, splits);
     return hipGetLastError();
 }
 
