@@ -268,9 +268,13 @@ __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear
 // ----------------------------------------------------------- many tokens
 // A workgroup computes RQ quads x TT 16-token tiles; its WR x WT waves own
 // RQ / WR quads x TT / WT tiles each.  Per 128-k chunk both operands go from
-// global memory straight to LDS, in operand order: A as the tile layout has
-// it, B as [tile][piece][token][16 bytes], so that every operand read is a
-// contiguous 1 KB per wave, free of bank conflicts.  On the FP8 matrix cores
+// global memory straight to LDS: A as the tile layout has it, B as token rows
+// of 128 bytes with 16-byte piece p of token c in slot p ^ (c / 2 % 8), so
+// that the 16 lanes of an operand read cover all banks.  A load of B takes 8
+// whole rows: with the rows' pieces spread over the lanes in operand order
+// instead (16 rows x 64 bytes per load) every quarter of a wave touches 16
+// cache lines, and the loads alone took 1.55 us a chunk against 0.6.  On the
+// FP8 matrix cores
 // (v_mfma_scale_f32_16x16x128_f8f6f4): lane (r, g) of an operand holds the
 // 16-byte pieces g and g + 4 of row r's 128 bytes and the scale of block g.
 template <int RQ, int TT, int STAGES>
@@ -316,9 +320,8 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
     }
 #pragma unroll
     for (int i = 0; i < kB; i++) {
-        const int piece = w * kB + i;  // tile piece / 2, pieces 4 (piece % 2) .. +3 of 16 tokens
-        const int64_t tok = t0 + min(piece / 2 * 16 + c, last);
-        srcB[i] = a.x_codes + tok * a.inner + (int64_t)k0 * 128 + (piece % 2) * 64 + g * 16;
+        const int row = (w * kB + i) * 8 + lane / 8;  // eight token rows per load
+        srcB[i] = a.x_codes + (t0 + min(row, last)) * a.inner + (int64_t)k0 * 128 + ((lane % 8) ^ (row / 2 % 8)) * 16;
     }
     if (w < RQ) {
         srcS = a.w_scales + ((int64_t)min(q0 + w, quads - 1) * chunks + k0) * 256 + lane * 4;
@@ -350,6 +353,7 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
     issue(k0, 0);
     int buf = 0;
     const int a_lo = (g & 1) * 1024 + (c + 16 * (g >> 1)) * 16;  // piece g; piece g + 4 is 512 bytes on
+    const int b_lo = c * 128 + (g ^ (c / 2)) * 16;               // piece g; piece g + 4 is in slot ^ 4
     for (int k = k0; k < k1; k++) {
         // this wave's loads of chunk k have landed; after the barrier every
         // wave's have, and every wave is done reading the other buffer
@@ -360,8 +364,8 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             const int tile = wt * NT + t;
-            B[t] = operand(*reinterpret_cast<const uint4*>(&sm.b[buf][tile][lane * 16]),
-                           *reinterpret_cast<const uint4*>(&sm.b[buf][tile][1024 + lane * 16]));
+            B[t] = operand(*reinterpret_cast<const uint4*>(&sm.b[buf][tile][b_lo]),
+                           *reinterpret_cast<const uint4*>(&sm.b[buf][tile][b_lo ^ 64]));
             sb[t] = reinterpret_cast<const uint8_t*>(&sm.bs[buf][tile * 16 + c])[g];
         }
 #pragma unroll
