@@ -40,4 +40,30 @@ __device__ inline void dma4(const uint8_t* src, uint32_t lds) {
         : "memory");
 }
 
+// The same with a scalar base address and a 32-bit offset per lane.  No
+// memory clobber: the loop's own wait and barrier orders them, and the
+// compiler may keep them among its other work.
+__device__ inline void dma16s(const uint8_t* base, uint32_t off, uint32_t lds) {
+    uint32_t save;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %3\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %1, %2\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(save)
+        : "v"(off), "s"(base), "s"(lds));
+}
+__device__ inline void dma4s(const uint8_t* base, uint32_t off, uint32_t lds) {
+    uint32_t save;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %3\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %1, %2\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(save)
+        : "v"(off), "s"(base), "s"(lds));
+}
+
 }  // namespace moe

@@ -3,8 +3,7 @@
 // The weights come in the MXFP8 tile layout of moe_mxfp8_prepack (prepack.hip):
 // per 64-row quad and 128-k chunk 8 KB of codes [group][half][lane][16] and
 // 256 scale bytes [lane][group], lane (r, g) = (l % 16, l / 16) holding block
-// g (k = 32g .. 32g+31) of row r.  D of a 16x16 product: lane (c, g) holds
-// rows 4g .. 4g+3 of token c.
+// g (k = 32g .. 32g+31) of row r.
 //
 // Few tokens (linear_rows_kernel): the weights' bytes bound the call.  Both
 // operands are decoded to bf16 (exact: E4M3 has four significant bits, the
@@ -13,11 +12,17 @@
 // bits below about 2^-16 of the largest product of a group (measured: 1.4e-5
 // of the sum's rms against 4e-8), and at these sizes their rate is not
 // needed.
-#include "../lds_dma.h"
+// Many tokens (linear_tile_kernel): the FP8 matrix cores, tiles of up to
+// 256 x 256 staged through LDS.
+// Either may split the inner axis over workgroups that leave float32 sums in
+// the workspace for linear_finish_kernel.
+#include "lds_dma.h"
 #include "ops_internal.h"
 
 namespace moe {
 namespace {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 __device__ inline i32x8_t operand(const uint4& lo, const uint4& hi) {
     return i32x8_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
@@ -25,147 +30,152 @@ __device__ inline i32x8_t operand(const uint4& lo, const uint4& hi) {
 
 // v / (1 + exp(-v)); the hardware exponential and reciprocal (about 1 ulp each)
 __device__ inline float silu(float v) { return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
-// erfc keeps the relative precision of the left tail that 1 + erf loses
-__device__ inline float gelu(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
 
-// What a lane does with the sums of G 16-row groups of one quad and one token:
-// acc[i][j] = row 4 g + j of group `group(i)`: the groups are sub * G + i,
-// or, with gate/up pairs (groups 0, 1 gate and 2, 3 up rows) and G = 2, gate
-// group sub and up group sub + 2.  Every lane of the wave takes part (the
-// MXFP8 block scales need the four lanes of a token); `live` lanes store.
-// MXFP8 output takes whole blocks of 32 columns: G >= 2, gated G = 4.
-template <int G>
-__device__ inline void finish(const moe_mxfp8_linear_args& a, int64_t quad, int sub, int64_t t, bool live,
-                              f32x4_t (&acc)[G]) {
-    const int g = (threadIdx.x % kWave) / 16;
-    const bool gated = a.activation == MOE_EPI_SILU_MUL;
-    if (a.bias) {
-#pragma unroll
-        for (int i = 0; i < G; i++) {
-            const int h = G / 2;  // gated: groups i >= h are up rows
-            const int64_t row = gated ? (i < h ? 0 : a.rows / 2) + 32 * quad + 16 * (sub * h + (h ? i % h : 0))
-                                      : 64 * quad + 16 * (sub * G + i);
-            const float4 b = *reinterpret_cast<const float4*>(a.bias + row + 4 * g);
-            acc[i] += f32x4_t{b.x, b.y, b.z, b.w};
-        }
-    }
-    int groups = G;  // 16-column groups of output, from column c0
-    int64_t c0 = 64 * quad + 16 * sub * G, cols = a.rows;
-    if (gated) {
-        groups = G / 2;
-        c0 = 32 * quad + 16 * sub * (G / 2);
-        cols = a.rows / 2;
-#pragma unroll
-        for (int i = 0; i < G / 2; i++)
-#pragma unroll
-            for (int j = 0; j < 4; j++) acc[i][j] = silu(acc[i][j]) * acc[i + G / 2][j];
-    } else if (a.activation == MOE_EPI_SILU) {
-#pragma unroll
-        for (int i = 0; i < G; i++)
-#pragma unroll
-            for (int j = 0; j < 4; j++) acc[i][j] = silu(acc[i][j]);
-    } else if (a.activation == MOE_EPI_GELU) {
-#pragma unroll
-        for (int i = 0; i < G; i++)
-#pragma unroll
-            for (int j = 0; j < 4; j++) acc[i][j] = gelu(acc[i][j]);
-    }
-    if (a.residual && live) {
-        const uint16_t* r = (const uint16_t*)a.residual + t * a.residual_stride + c0 + 4 * g;
-#pragma unroll
-        for (int i = 0; i < G; i++) {
-            if (i >= groups) break;
-            float v[4];
-            load_piece<4>(r + 16 * i, v);
-#pragma unroll
-            for (int j = 0; j < 4; j++) acc[i][j] += v[j];
-        }
-    }
-    if (a.out) {
-        if (!live) return;
-        uint16_t* o = (uint16_t*)a.out + t * a.out_stride + c0 + 4 * g;
-#pragma unroll
-        for (int i = 0; i < G; i++) {
-            if (i >= groups) break;
-            const float v[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
-            store_piece<4>(o + 16 * i, v);
-        }
-        return;
-    }
-    if constexpr (G >= 2) {
-#pragma unroll
-        for (int b = 0; b < G / 2; b++) {  // blocks of 32 columns: groups 2b, 2b + 1
-            if (2 * b >= groups) break;
-            uint32_t top = 0;
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) top = max(top, __float_as_uint(acc[2 * b + h][j]) & 0x7fffffffu);
-            top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-            top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-            const bool bad = top >= 0x7f800000u;
-            const int se = mxfp8_scale_exp(top);
-            if (!live) continue;
-            uint8_t* o = a.out_codes + t * cols + c0 + 32 * b + 4 * g;
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                float q[4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) q[j] = bad ? 0.f : ldexpf(acc[2 * b + h][j], -se);
-                *reinterpret_cast<uint32_t*>(o + 16 * h) = e4m3_pack4(q);
-            }
-            if (g == 0) a.out_scales[t * (cols / 32) + c0 / 32 + b] = bad ? 255 : (uint8_t)(se + 127);
-        }
-    }
+// v / 2 * (1 + erf(v / sqrt 2)) = v / 2 * erfc(-v / sqrt 2): erfc keeps the
+// relative precision of the left tail that 1 + erf loses.  For a >= 0,
+// erfc(a) = t exp(-a^2) f(t) with t = 1 / (1 + 0.4 a); f is a least-squares
+// polynomial for f(t) = erfc(a) exp(a^2) / t, weighted towards the smallest
+// largest relative error (2e-8, with float32 roundings 1.5e-7).
+__device__ inline float gelu(float v) {
+    const float a = fabsf(v) * 0.70710678118654752f;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.4f, a, 1.0f));
+    float f = -0.0224578306f;
+    f = fmaf(f, t, 0.160047933f);
+    f = fmaf(f, t, -0.411607653f);
+    f = fmaf(f, t, 0.43421036f);
+    f = fmaf(f, t, -0.193026885f);
+    f = fmaf(f, t, 0.224716902f);
+    f = fmaf(f, t, 0.14541091f);
+    f = fmaf(f, t, 0.211696655f);
+    f = fmaf(f, t, 0.225320622f);
+    f = fmaf(f, t, 0.225688994f);
+    const float r = t * f * __expf(-a * a);
+    return 0.5f * v * (v > 0.f ? 2.0f - r : r);
 }
 
-// A split of the inner axis leaves float32 sums in the workspace, one float4
-// per lane in the order the lanes hold them: [split][token tile][group][lane].
-__device__ inline float4* partial_of(const moe_mxfp8_linear_args& a, int split, int64_t tile, int64_t group) {
-    const int64_t tiles = (a.num_tokens + 15) / 16;
-    return (float4*)a.workspace + ((split * tiles + tile) * (a.rows / 16) + group) * kWave + threadIdx.x % kWave;
+// ------------------------------------------------------------- the output
+// A lane finishes 8 consecutive columns of one token: v holds their sums,
+// and with gate/up pairs u those of the up rows.
+
+__device__ inline void add8(float (&v)[8], const float* p) {  // 16-byte aligned
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+    v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
 }
 
-// one wave per (quad, 16-token tile): the splits' sums in order, then finish
-__global__ void __launch_bounds__(256) linear_finish_kernel(moe_mxfp8_linear_args a, int splits) {
-    const int64_t quads = a.rows / 64, unit = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
-    const int64_t quad = unit % quads, tile = unit / quads;
-    if (16 * tile >= a.num_tokens) return;
-    f32x4_t acc[4];
+__device__ inline uint4 residual8(const moe_mxfp8_linear_args& a, int64_t t, int64_t c0) {
+    return *reinterpret_cast<const uint4*>((const uint16_t*)a.residual + t * a.residual_stride + c0);
+}
+
+// the largest of v over the four lanes of a quad (a block of 32 columns)
+__device__ inline uint32_t quad_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xf, 0xf, true));  // lanes 1, 0, 3, 2
+    return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xf, 0xf, true));  // lanes 2, 3, 0, 1
+}
+
+// columns c0 .. c0+7 of token t (live lanes store; whole quads of lanes take
+// part).  act and mx are constants where the caller's are.
+__device__ inline void finish8(const moe_mxfp8_linear_args& a, int act, bool mx, int64_t cols, int64_t t, int64_t c0,
+                               bool live, float (&v)[8], const float (&u)[8], const uint4& res) {
+    if (act == MOE_EPI_SILU_MUL) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; s++)
+        for (int i = 0; i < 8; i++) v[i] = silu(v[i]) * u[i];
+    } else if (act == MOE_EPI_SILU) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = silu(v[i]);
+    } else if (act == MOE_EPI_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = gelu(v[i]);
+    }
+    if (a.residual) {
+        const uint32_t w[4] = {res.x, res.y, res.z, res.w};
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const float4 v = *partial_of(a, s, tile, 4 * quad + i);
-            acc[i] += f32x4_t{v.x, v.y, v.z, v.w};
+            v[2 * i] += __uint_as_float(w[i] << 16);
+            v[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
         }
-    const int64_t t = 16 * tile + threadIdx.x % 16;
-    finish<4>(a, quad, 0, t, t < a.num_tokens, acc);
+    }
+    if (!mx) {
+        if (live) store_piece<8>((uint16_t*)a.out + t * a.out_stride + c0, v);
+        return;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    top = quad_max(top);
+    const bool bad = top >= 0x7f800000u;
+    const int se = mxfp8_scale_exp(top);
+    if (!live) return;
+    uint32_t code[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        float q[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) q[i] = bad ? 0.f : ldexpf(v[4 * h + i], -se);
+        code[h] = e4m3_pack4(q);
+    }
+    *reinterpret_cast<uint2*>(a.out_codes + t * cols + c0) = make_uint2(code[0], code[1]);
+    if (c0 % 32 == 0) a.out_scales[t * (cols / 32) + c0 / 32] = bad ? 255 : (uint8_t)(se + 127);
+}
+
+// A split of the inner axis leaves float32 sums in the workspace,
+// [split][token][row], rows in the tile layout's order (with gate/up pairs:
+// 32 gate, then 32 up rows per quad).
+__device__ inline float* partial_of(const moe_mxfp8_linear_args& a, int split, int64_t t, int64_t row) {
+    return (float*)a.workspace + (split * a.num_tokens + t) * a.rows + row;
+}
+
+// one lane per (token, 8 columns): the splits' sums in order, then finish8
+__global__ void __launch_bounds__(256) linear_finish_kernel(moe_mxfp8_linear_args a, int splits) {
+    const bool gated = a.activation == MOE_EPI_SILU_MUL;
+    const int64_t cols = gated ? a.rows / 2 : a.rows, octs = cols / 8;
+    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const bool live = idx < a.num_tokens * octs;
+    const int64_t t = live ? idx / octs : a.num_tokens - 1, o = live ? idx % octs : octs - 1;
+    const int64_t row = gated ? o / 4 * 64 + o % 4 * 8 : o * 8;
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if (a.residual) res = residual8(a, t, 8 * o);
+    float v[8] = {}, u[8] = {};
+    for (int s = 0; s < splits; s++) {
+        add8(v, partial_of(a, s, t, row));
+        if (gated) add8(u, partial_of(a, s, t, row + 32));
+    }
+    if (a.bias) {
+        add8(v, a.bias + 8 * o);
+        if (gated) add8(u, a.bias + cols + 8 * o);
+    }
+    finish8(a, a.activation, a.out_codes != nullptr, cols, t, 8 * o, live, v, u, res);
 }
 
 // ------------------------------------------------------------ few tokens
 // A workgroup of W waves owns G 16-row groups of a quad and NT 16-token
-// tiles; its waves take the chunks of its part of the inner axis in turn and
-// add their sums in LDS, in wave order.  Weights and tokens go straight from
-// global memory to registers (a tile-layout load is a contiguous 1 KB per
-// wave), one chunk ahead.
-template <int G, int NT>
-struct RowsChunk {
-    u32x4_t a[G][2], b[NT][2];
-    uint32_t sa, sb[NT];
-};
+// tiles; each wave takes a run of the chunks of the workgroup's part of the
+// inner axis, and the waves' sums meet in LDS, added in wave order.  Weights
+// go from global memory to registers (a tile-layout load is a contiguous 1 KB
+// per wave), token rows through the wave's own LDS, as whole 128-byte lines
+// (16 rows x 16 bytes per quarter wave, which the operand order would give,
+// cost a cache access per lane); both two chunks ahead.
+constexpr int kSegment = 16;  // chunks whose token scales a wave holds in LDS
 
 struct RowsGrid {
     int units, groups;          // weight units (rows / 16G), token groups of NT tiles
     int splits, split_chunks;   // parts of the inner axis, chunks of one
 };
 
+template <int NT>
+struct RowsWave {  // one wave's staged tokens
+    alignas(16) uint8_t x[2][NT][16 * 128];            // rows of 128 bytes, piece p of row c in slot p ^ (c / 2 % 8)
+    alignas(16) uint8_t s[NT][kSegment / 4][16 * 16];  // scale bytes [row][4 chunks][4 blocks]
+};
+
 template <int G, int NT, int W>
 __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear_args a, RowsGrid p) {
-    __shared__ f32x4_t red[W][NT * G][kWave];
-    constexpr bool kPaired = G == 2;
-    const int w = threadIdx.x / kWave, lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
+    union Smem {
+        RowsWave<NT> wave[W];
+        float sum[W][NT * 16][16 * G + 4];  // [wave][token][row], padded
+    };
+    __shared__ Smem sm;
+    const int w = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
     // the token groups of a unit run on one XCD (workgroups go round the
     // eight), where its weights come from HBM once
     const int per_split = 8 * p.groups * ((p.units + 7) / 8);
@@ -176,113 +186,161 @@ __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear
     const int sub = unit % (4 / G);
     const int chunks = (int)(a.inner / 128);
     const int k0 = split * p.split_chunks, k1 = min(chunks, k0 + p.split_chunks);
-    const bool gated = kPaired && a.activation == MOE_EPI_SILU_MUL;
-    int group[G];
+    const int run = (k1 - k0 + W - 1) / W, r0 = k0 + w * run, r1 = min(k1, r0 + run);  // this wave's chunks
+    const bool gated = a.activation == MOE_EPI_SILU_MUL;
+    int group[G];  // the 16-row groups of the quad; G = 2 pairs a gate group with its up group
 #pragma unroll
-    for (int i = 0; i < G; i++) group[i] = gated ? sub + 2 * i : sub * G + i;
+    for (int i = 0; i < G; i++) group[i] = G == 2 && gated ? sub + 2 * i : sub * G + i;
     const uint8_t* wt = a.w_tiles + quad * chunks * 8192 + lane * 16;
     const uint8_t* ws = a.w_scales + quad * chunks * 256 + lane * 4;
-    const uint8_t *xr[NT], *xs[NT];
+    const int64_t t0 = (int64_t)tg * (16 * NT);
+    const int last = (int)min((int64_t)(16 * NT), a.num_tokens - t0) - 1;  // rows past it repeat it
+    const uint8_t *xr[NT][2], *xs[NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        const int64_t tok = min((int64_t)(16 * (tg * NT + t) + c), a.num_tokens - 1);
-        xr[t] = a.x_codes + tok * a.inner + 32 * g;
-        xs[t] = a.x_scales + tok * (a.inner / 32) + g;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int row = 8 * h + lane / 8;
+            xr[t][h] = a.x_codes + (t0 + min(16 * t + row, last)) * a.inner + ((lane % 8) ^ (row / 2)) * 16;
+        }
+        xs[t] = a.x_scales + (t0 + min(16 * t + lane / 4, last)) * (a.inner / 32);
     }
+    RowsWave<NT>& mine = sm.wave[w];
     f32x4_t acc[NT][G];
 #pragma unroll
     for (int t = 0; t < NT; t++)
 #pragma unroll
         for (int i = 0; i < G; i++) acc[t][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    // loads are unconditional (chunks past the end repeat the last one and
-    // are not multiplied): the compiler then waits for exactly what it uses
-    auto load = [&](RowsChunk<G, NT>& r, int k) {
-        const int ch = min(k, k1 - 1);
-        r.sa = *reinterpret_cast<const uint32_t*>(ws + (int64_t)ch * 256);
+    struct Weights {
+        u32x4_t v[G][2];
+        uint32_t s;
+    } wb[2];
+    // chunk k (one past the run repeats its last one and is not used)
+    auto load = [&](Weights& r, int k, int buf) {
+        const int ch = min(k, r1 - 1);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what was read of this buffer has arrived
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) dma16(xr[t][h] + ch * 128, lds_addr(&mine.x[buf][t][1024 * h]));
+        r.s = *reinterpret_cast<const uint32_t*>(ws + (int64_t)ch * 256);
 #pragma unroll
         for (int i = 0; i < G; i++)
 #pragma unroll
             for (int h = 0; h < 2; h++)
-                r.a[i][h] = __builtin_nontemporal_load(
+                r.v[i][h] = __builtin_nontemporal_load(
                     reinterpret_cast<const u32x4_t*>(wt + (int64_t)ch * 8192 + group[i] * 2048 + h * 1024));
+    };
+    constexpr int kLoads = 2 * NT + 1 + 2 * G;  // of one chunk
+    auto multiply = [&](const Weights& r, int k, int buf) {
+        uint4 xb[NT][2];
+        uint32_t sb[NT];
 #pragma unroll
         for (int t = 0; t < NT; t++) {
-            r.sb[t] = xs[t][ch * 4];
 #pragma unroll
             for (int h = 0; h < 2; h++)
-                r.b[t][h] = *reinterpret_cast<const u32x4_t*>(xr[t] + ch * 128 + 16 * h);
+                xb[t][h] = *reinterpret_cast<const uint4*>(&mine.x[buf][t][c * 128 + ((2 * g + h) ^ (c / 2)) * 16]);
+            sb[t] = mine.s[t][k % kSegment / 4][c * 16 + k % 4 * 4 + g];
         }
-    };
-    auto multiply = [&](const RowsChunk<G, NT>& r) {
 #pragma unroll
         for (int q = 0; q < 4; q++) {  // k = 32 g + 8 q .. + 7 of each lane group
             bf16x8_t B[NT];
 #pragma unroll
-            for (int t = 0; t < NT; t++)
-                B[t] = decode8_e4m3(r.b[t][q / 2][2 * (q % 2)], r.b[t][q / 2][2 * (q % 2) + 1],
-                                    e8m0_as_scale(r.sb[t]));
+            for (int t = 0; t < NT; t++) {
+                const uint4& v = xb[t][q / 2];
+                B[t] = q % 2 ? decode8_e4m3(v.z, v.w, e8m0_as_scale(sb[t])) : decode8_e4m3(v.x, v.y, e8m0_as_scale(sb[t]));
+            }
 #pragma unroll
             for (int i = 0; i < G; i++) {
-                const bf16x8_t A = decode8_e4m3(r.a[i][q / 2][2 * (q % 2)], r.a[i][q / 2][2 * (q % 2) + 1],
-                                                e8m0_as_scale((r.sa >> (8 * group[i])) & 0xffu));
+                const bf16x8_t A = decode8_e4m3(r.v[i][q / 2][2 * (q % 2)], r.v[i][q / 2][2 * (q % 2) + 1],
+                                                e8m0_as_scale((r.s >> (8 * group[i])) & 0xffu));
 #pragma unroll
                 for (int t = 0; t < NT; t++)
                     acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B[t], acc[t][i], 0, 0, 0);
             }
         }
     };
-    RowsChunk<G, NT> r0, r1;
-    load(r0, k0 + w);
-    for (int k = k0 + w; k < k1; k += 2 * W) {
-        load(r1, k + W);
-        multiply(r0);
-        load(r0, k + 2 * W);
-        if (k + W < k1) multiply(r1);
+    for (int seg = r0; seg < r1; seg += kSegment) {  // k % kSegment counts from the segment's start
+        const int n = min(kSegment, r1 - seg);
+        for (int j = 0; j < (n + 3) / 4; j++)
+#pragma unroll
+            for (int t = 0; t < NT; t++)
+                dma4(xs[t] + min(seg + 4 * j + lane % 4, r1 - 1) * 4, lds_addr(&mine.s[t][j][0]));
+        load(wb[0], seg, 0);
+        load(wb[1], seg + 1, 1);
+        for (int i = 0; i < n; i += 2) {
+            // the wave's own loads of chunk i have landed (those of i + 1 may be in flight)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+            multiply(wb[0], i, 0);
+            load(wb[0], seg + i + 2, 0);
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+            if (i + 1 < n) multiply(wb[1], i + 1, 1);
+            load(wb[1], seg + i + 3, 1);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < NT; t++)
 #pragma unroll
-        for (int i = 0; i < G; i++) red[w][t * G + i][lane] = acc[t][i];
+        for (int i = 0; i < G; i++)
+            *reinterpret_cast<f32x4_t*>(&sm.sum[w][16 * t + c][16 * i + 4 * g]) = acc[t][i];
     __syncthreads();
-    for (int t = w; t < NT; t += W) {
-        const int64_t tile = tg * NT + t;
-        if (16 * tile >= a.num_tokens) break;
-        f32x4_t v[G];
-#pragma unroll
-        for (int i = 0; i < G; i++) {
-            v[i] = red[0][t * G + i][lane];
-#pragma unroll
-            for (int u = 1; u < W; u++) v[i] += red[u][t * G + i][lane];
-        }
+    // one lane per (token, 8 columns)
+    const int octs = gated && p.splits == 1 ? G : 2 * G;
+    const int64_t cols = gated ? a.rows / 2 : a.rows;
+    for (int idx = threadIdx.x; idx < NT * 16 * octs; idx += W * kWave) {
+        const int tok = idx / octs, o = idx % octs;
+        const int64_t t = t0 + tok;
+        const bool live = tok <= last;
         if (p.splits > 1) {
+            float v[8] = {};
 #pragma unroll
-            for (int i = 0; i < G; i++)
-                *partial_of(a, split, tile, 4 * quad + group[i]) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-        } else {
-            const int64_t tok = 16 * tile + c;
-            finish<G>(a, quad, sub, tok, tok < a.num_tokens, v);
+            for (int u = 0; u < W; u++) add8(v, &sm.sum[u][tok][8 * o]);
+            // groups in order (G = 4, or a gate/up pair half a quad apart)
+            const int64_t row = 64 * quad + 16 * group[0] + (G == 2 && gated ? o / 2 * 32 + o % 2 * 8 : 8 * o);
+            float* d = partial_of(a, split, live ? t : a.num_tokens - 1, row);
+            if (live) store_piece<8>(d, v);
+            continue;
         }
+        const int64_t c0 = gated ? 32 * quad + 16 * sub * (G / 2) + 8 * o : 64 * quad + 16 * sub * G + 8 * o;
+        uint4 res = make_uint4(0, 0, 0, 0);
+        if (a.residual) res = residual8(a, live ? t : a.num_tokens - 1, c0);
+        float v[8] = {}, u[8] = {};
+#pragma unroll
+        for (int i = 0; i < W; i++) add8(v, &sm.sum[i][tok][8 * o]);
+        if (gated)
+#pragma unroll
+            for (int i = 0; i < W; i++) add8(u, &sm.sum[i][tok][8 * G + 8 * o]);
+        if (a.bias) {
+            add8(v, a.bias + c0);
+            if (gated) add8(u, a.bias + cols + c0);
+        }
+        finish8(a, a.activation, a.out_codes != nullptr, cols, t, c0, live, v, u, res);
     }
 }
 
 // ----------------------------------------------------------- many tokens
-// A workgroup computes RQ quads x TT 16-token tiles; its WR x WT waves own
+// A workgroup computes RQ quads x TT 32-token tiles; its WR x WT waves own
 // RQ / WR quads x TT / WT tiles each.  Per 128-k chunk both operands go from
 // global memory straight to LDS: A as the tile layout has it, B as token rows
 // of 128 bytes with 16-byte piece p of token c in slot p ^ (c / 2 % 8), so
-// that the 16 lanes of an operand read cover all banks.  A load of B takes 8
-// whole rows: with the rows' pieces spread over the lanes in operand order
+// that the 16 lanes of a quarter wave read all banks once.  A load of B takes
+// 8 whole rows: with the rows' pieces spread over the lanes in operand order
 // instead (16 rows x 64 bytes per load) every quarter of a wave touches 16
-// cache lines, and the loads alone took 1.55 us a chunk against 0.6.  On the
-// FP8 matrix cores
-// (v_mfma_scale_f32_16x16x128_f8f6f4): lane (r, g) of an operand holds the
-// 16-byte pieces g and g + 4 of row r's 128 bytes and the scale of block g.
+// cache lines, and the loads alone took 1.55 us a chunk against 0.6.
+// Products: v_mfma_scale_f32_32x32x64_f8f6f4, two per chunk (s = 0, 1).
+// Lane (r, h) = (l % 32, l / 32) of an operand holds the 16-byte pieces
+// 4s + h and 4s + h + 2 of row r's 128 bytes and the scale of block 2s + h;
+// of D rows 8j + 4h .. + 3 (j = 0 .. 3) of token r.
 template <int RQ, int TT, int STAGES>
 struct TileSmem {
     alignas(16) uint8_t a[STAGES][RQ][8192];
-    alignas(16) uint8_t b[STAGES][TT][2048];
-    alignas(16) uint32_t as[STAGES][RQ][kWave];
-    alignas(16) uint32_t bs[STAGES][TT * 16];
+    alignas(16) uint8_t b[STAGES][TT][4096];
+    struct {
+        alignas(16) uint32_t a[RQ][kWave];
+        alignas(16) uint32_t b[TT * 32];
+    } s[STAGES];  // the block scales
 };
 
 struct TileGrid {
@@ -290,131 +348,196 @@ struct TileGrid {
     int splits, split_chunks;
 };
 
-template <int RQ, int TT, int WR, int WT>
+template <int SA, int SB>
+__device__ inline f32x16_t mfma32(const i32x8_t& A, const i32x8_t& B, const f32x16_t& c, uint32_t sa, uint32_t sb) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 0, 0, SA, (int)sa, SB, (int)sb);
+}
+
+template <int ACT, bool MX, int RQ, int TT, int WR, int WT>
 __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_linear_args a, TileGrid p) {
     constexpr int kStages = 2, kWaves = WR * WT;
-    constexpr int Q = RQ / WR, NT = TT / WT;              // a wave's quads and token tiles
-    constexpr int kA = RQ * 8 / kWaves, kB = TT * 2 / kWaves;  // 1 KB loads per wave and chunk
-    static_assert(RQ * 8 % kWaves == 0 && TT * 2 % kWaves == 0 && RQ + TT / 4 == kWaves, "loads per wave");
+    constexpr int Q = RQ / WR, NT = TT / WT;                   // a wave's quads and token tiles
+    constexpr int kA = RQ * 8 / kWaves, kB = TT * 4 / kWaves;  // 1 KB loads per wave and chunk
+    static_assert(RQ * 8 % kWaves == 0 && TT * 4 % kWaves == 0 && RQ + TT / 2 == kWaves, "loads per wave");
     extern __shared__ uint8_t smem_raw[];
     auto& sm = *reinterpret_cast<TileSmem<RQ, TT, kStages>*>(smem_raw);
-    const int w = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
+    const int w = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, c = lane % 32, h = lane / 32;
     const int per_split = p.row_blocks * p.tok_blocks;
     const int split = blockIdx.x / per_split, blk = blockIdx.x % per_split;
     const int rb = blk % p.row_blocks, tb = blk / p.row_blocks;
     const int chunks = (int)(a.inner / 128), quads = (int)(a.rows / 64);
     const int k0 = split * p.split_chunks, k1 = min(chunks, k0 + p.split_chunks);
     const int q0 = rb * RQ;
-    const int64_t t0 = (int64_t)tb * (16 * TT);
-    const int last = (int)min((int64_t)(16 * TT), a.num_tokens - t0) - 1;  // rows past it repeat it
+    const int64_t t0 = (int64_t)tb * (32 * TT);
+    const int last = (int)min((int64_t)(32 * TT), a.num_tokens - t0) - 1;  // rows past it repeat it
 
-    // this wave's loads of chunk k0 (quads past the end repeat the last one)
-    const uint8_t* srcA[kA];
-    const uint8_t* srcB[kB];
-    const uint8_t* srcS;
-    int step_s;
+    // This wave's loads of a chunk: a scalar base that moves on by a fixed
+    // step per chunk, and a 32-bit offset per lane (tokens relative to the
+    // workgroup's first row).  Quads past the end repeat the last one.
+    const uint8_t* baseA[kA];
+    uint32_t offB[kB];
 #pragma unroll
     for (int i = 0; i < kA; i++) {
         const int piece = w * kA + i;  // quad piece / 8, 1 KB piece % 8
-        srcA[i] = a.w_tiles + ((int64_t)min(q0 + piece / 8, quads - 1) * chunks + k0) * 8192 + piece % 8 * 1024 + lane * 16;
+        baseA[i] = a.w_tiles + ((int64_t)min(q0 + piece / 8, quads - 1) * chunks + k0) * 8192 + piece % 8 * 1024;
     }
 #pragma unroll
     for (int i = 0; i < kB; i++) {
         const int row = (w * kB + i) * 8 + lane / 8;  // eight token rows per load
-        srcB[i] = a.x_codes + (t0 + min(row, last)) * a.inner + (int64_t)k0 * 128 + ((lane % 8) ^ (row / 2 % 8)) * 16;
+        offB[i] = (uint32_t)min(row, last) * (uint32_t)a.inner + ((lane % 8) ^ (row / 2 % 8)) * 16;
     }
+    const uint8_t* baseB = a.x_codes + t0 * a.inner + (int64_t)k0 * 128;
+    const uint8_t* baseS;
+    uint32_t offS;
+    int step_s;
     if (w < RQ) {
-        srcS = a.w_scales + ((int64_t)min(q0 + w, quads - 1) * chunks + k0) * 256 + lane * 4;
+        baseS = a.w_scales + ((int64_t)min(q0 + w, quads - 1) * chunks + k0) * 256;
+        offS = lane * 4;
         step_s = 256;
     } else {
-        const int64_t tok = t0 + min((w - RQ) * kWave + lane, last);
-        srcS = a.x_scales + tok * (a.inner / 32) + (int64_t)k0 * 4;
+        baseS = a.x_scales + t0 * (a.inner / 32) + (int64_t)k0 * 4;
+        offS = (uint32_t)min((w - RQ) * kWave + lane, last) * (uint32_t)(a.inner / 32);
         step_s = 4;
     }
-    auto issue = [&](int k, int buf) {
-        const int d = k - k0;
-#pragma unroll
-        for (int i = 0; i < kA; i++)
-            dma16(srcA[i] + (int64_t)d * 8192, lds_addr(&sm.a[buf][0][(w * kA + i) * 1024]));
-#pragma unroll
-        for (int i = 0; i < kB; i++)
-            dma16(srcB[i] + d * 128, lds_addr(&sm.b[buf][0][(w * kB + i) * 1024]));
-        dma4(srcS + (int64_t)d * step_s, lds_addr(w < RQ ? (const void*)&sm.as[buf][w][0]
-                                                        : (const void*)&sm.bs[buf][(w - RQ) * kWave]));
+    const uint32_t lds = lds_addr(smem_raw);
+    constexpr uint32_t kBufA = RQ * 8192, kBufB = TT * 4096, kBufS = (RQ * kWave + TT * 32) * 4;
+    constexpr uint32_t kAtB = kStages * kBufA, kAtS = kAtB + kStages * kBufB;
+    const uint32_t ldsS = lds + kAtS + w * (kWave * 4);
+    // load n of the kLoads of this wave's next chunk, into buffer buf
+    constexpr int kLoads = kA + kB + 1;
+    auto issue = [&](auto n, int buf) {
+        constexpr int i = decltype(n)::value;
+        if constexpr (i < kB) {
+            dma16s(baseB, offB[i], lds + kAtB + buf * kBufB + (w * kB + i) * 1024);
+            if constexpr (i == kB - 1) baseB += 128;
+        } else if constexpr (i < kB + kA) {
+            dma16s(baseA[i - kB], lane * 16, lds + buf * kBufA + (w * kA + i - kB) * 1024);
+            baseA[i - kB] += 8192;
+        } else {
+            dma4s(baseS, offS, ldsS + buf * kBufS);
+            baseS += step_s;
+        }
     };
     const int wr = w % WR, wt = w / WR;
-    f32x4_t acc[Q][4][NT];
+    f32x16_t acc[2 * Q][NT];
 #pragma unroll
-    for (int q = 0; q < Q; q++)
+    for (int i = 0; i < 2 * Q; i++)
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int t = 0; t < NT; t++) acc[q][i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    issue(k0, 0);
+        for (int t = 0; t < NT; t++) acc[i][t] = f32x16_t{};
+    static_for<kLoads>([&](auto n) { issue(n, 0); });
     int buf = 0;
-    const int a_lo = (g & 1) * 1024 + (c + 16 * (g >> 1)) * 16;  // piece g; piece g + 4 is 512 bytes on
-    const int b_lo = c * 128 + (g ^ (c / 2)) * 16;               // piece g; piece g + 4 is in slot ^ 4
-    for (int k = k0; k < k1; k++) {
-        // this wave's loads of chunk k have landed; after the barrier every
-        // wave's have, and every wave is done reading the other buffer
-        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-        if (k + 1 < k1) issue(k + 1, buf ^ 1);
-        i32x8_t B[NT];
+    // A: row r of 32 is row r % 16 of group r / 16; piece 4s + h (then + 2) is
+    // half h, lane r % 16 + 32 s (then + 16).  Its scale byte is that of the
+    // group: the odd group's is shifted down to the even one's place.
+    const int r = c % 16, a_at = c / 16 * 2048 + h * 1024 + r * 16, as_at = r + 16 * h, as_shift = c / 16 * 8;
+    const int b_at = c * 128 + (h ^ (c / 2 % 8)) * 16;
+    auto step = [&](auto more) {
+        // this wave's loads of the chunk have landed; after the barrier every
+        // wave's have, and every wave has what it read of the other buffer
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         uint32_t sb[NT];
 #pragma unroll
-        for (int t = 0; t < NT; t++) {
-            const int tile = wt * NT + t;
-            B[t] = operand(*reinterpret_cast<const uint4*>(&sm.b[buf][tile][b_lo]),
-                           *reinterpret_cast<const uint4*>(&sm.b[buf][tile][b_lo ^ 64]));
-            sb[t] = reinterpret_cast<const uint8_t*>(&sm.bs[buf][tile * 16 + c])[g];
-        }
+        for (int t = 0; t < NT; t++) sb[t] = sm.s[buf].b[(wt * NT + t) * 32 + c] >> (8 * h);
+        static_for<2>([&](auto s) {
+            i32x8_t B[NT];
 #pragma unroll
-        for (int q = 0; q < Q; q++) {
-            const uint8_t* qa = &sm.a[buf][wr * Q + q][a_lo];
-            const uint32_t sa = sm.as[buf][wr * Q + q][lane];
-            static_for<4>([&](auto i) {
-                const i32x8_t A = operand(*reinterpret_cast<const uint4*>(qa + i * 2048),
-                                          *reinterpret_cast<const uint4*>(qa + i * 2048 + 512));
+            for (int t = 0; t < NT; t++) {
+                const uint8_t* row = sm.b[buf][wt * NT + t];
+                B[t] = operand(*reinterpret_cast<const uint4*>(row + (b_at ^ (64 * s))),
+                               *reinterpret_cast<const uint4*>(row + (b_at ^ (64 * s + 32))));
+            }
+            static_for<Q>([&](auto q) {
+                const uint8_t* qa = &sm.a[buf][wr * Q + q][a_at + 512 * s];
+                const uint32_t sa = sm.s[buf].a[wr * Q + q][as_at + 32 * s] >> as_shift;
+                static_for<2>([&](auto i) {
+                    const i32x8_t A = operand(*reinterpret_cast<const uint4*>(qa + i * 4096),
+                                              *reinterpret_cast<const uint4*>(qa + i * 4096 + 256));
 #pragma unroll
-                for (int t = 0; t < NT; t++) acc[q][i][t] = mfma_scaled<0, i, 0>(A, B[t], acc[q][i][t], sa, sb[t]);
+                    for (int t = 0; t < NT; t++)
+                        acc[2 * q + i][t] = mfma32<2 * decltype(i)::value, 2 * decltype(s)::value>(
+                            A, B[t], acc[2 * q + i][t], sa, sb[t]);
+                    // the next chunk's loads go out between the products
+                    constexpr int at = (decltype(s)::value * Q + decltype(q)::value) * 2 + decltype(i)::value;
+                    constexpr int per = (kLoads + 4 * Q - 1) / (4 * Q);
+                    if constexpr (decltype(more)::value)
+                        static_for<per>([&](auto j) {
+                            constexpr int n = at * per + decltype(j)::value;
+                            if constexpr (n < kLoads) issue(std::integral_constant<int, n>{}, buf ^ 1);
+                        });
+                });
             });
-        }
-        buf ^= 1;
-    }
-    // The sums leave through this wave's own part of the LDS (one quad x tile
-    // a time, in the lanes' own order), so that the epilogue is one piece of
-    // code in a loop instead of Q * NT copies of it.
-    __syncthreads();
-    constexpr int kUnits = Q * NT;
-    constexpr int kRound = sizeof(TileSmem<RQ, TT, kStages>) / (kWaves * 4096) < kUnits
-                               ? sizeof(TileSmem<RQ, TT, kStages>) / (kWaves * 4096) : kUnits;
-    f32x4_t(*mine)[4][kWave] = reinterpret_cast<f32x4_t(*)[4][kWave]>(smem_raw + w * kRound * 4096);
-    static_for<(kUnits + kRound - 1) / kRound>([&](auto round) {
-        static_for<kRound>([&](auto u) {
-            constexpr int n = decltype(round)::value * kRound + decltype(u)::value;
-            if constexpr (n < kUnits) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) mine[u][i][lane] = acc[n / NT][i][n % NT];
-            }
         });
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-        for (int u = 0; u < kRound; u++) {
-            const int n = round * kRound + u;
-            const int quad = q0 + wr * Q + n / NT;
-            const int64_t tile = (int64_t)tb * TT + wt * NT + n % NT;
-            if (n >= kUnits || quad >= quads || 16 * tile >= a.num_tokens) continue;
-            f32x4_t v[4];
+        buf ^= 1;
+    };
+    for (int k = k0; k + 1 < k1; k++) step(std::true_type{});
+    step(std::false_type{});
+
+    // The sums go through this wave's own part of the LDS, one token tile at
+    // a time, to lanes that hold 8 consecutive columns of a token: rows of 16
+    // lanes then read the residual and write the output in 256-byte runs.
+    constexpr bool kGated = ACT == MOE_EPI_SILU_MUL;
+    constexpr int kRow = 64 * Q + 4;                 // padded: 16-byte writes of 16 tokens cover all banks
+    constexpr int kOcts = kGated ? 4 * Q : 8 * Q;    // output octets of a token
+    constexpr int kItems = 32 * kOcts / kWave;       // per lane and token tile
+    static_assert(sizeof(TileSmem<RQ, TT, kStages>) >= kWaves * 32 * kRow * 4, "staging of the sums");
+    __syncthreads();  // every wave is done with the last chunk
+    float(*mine)[kRow] = reinterpret_cast<float(*)[kRow]>(smem_raw + w * (32 * kRow * 4));
+    const int64_t cols = kGated ? a.rows / 2 : a.rows;
+    const int wq = q0 + wr * Q;                      // this wave's first quad
+    const int64_t tw = t0 + wt * NT * 32;            // and first token
+    if (p.splits > 1) {
+        static_for<NT>([&](auto t) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) v[i] = mine[u][i][lane];
-            if (p.splits > 1) {
+            for (int i = 0; i < 2 * Q; i++)
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    *partial_of(a, split, tile, 4 * quad + i) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-            } else {
-                const int64_t t = 16 * tile + c;
-                finish<4>(a, quad, 0, t, t < a.num_tokens, v);
+                for (int j = 0; j < 4; j++)
+                    *reinterpret_cast<float4*>(&mine[c][32 * i + 8 * j + 4 * h]) =
+                        make_float4(acc[i][t][4 * j], acc[i][t][4 * j + 1], acc[i][t][4 * j + 2], acc[i][t][4 * j + 3]);
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll 2
+            for (int n = 0; n < 32 * 8 * Q / kWave; n++) {
+                const int idx = n * kWave + lane, tok = idx / (8 * Q), o = idx % (8 * Q);
+                float v[8] = {};
+                add8(v, &mine[tok][8 * o]);
+                if (tw + 32 * t + tok < a.num_tokens && wq + o / 8 < quads)
+                    store_piece<8>(partial_of(a, split, tw + 32 * t + tok, (int64_t)wq * 64 + 8 * o), v);
             }
+            __builtin_amdgcn_wave_barrier();
+        });
+        return;
+    }
+    const int o = lane % kOcts;
+    const int64_t c0 = (int64_t)wq * (kGated ? 32 : 64) + 8 * o;
+    const bool in = c0 < cols;
+    float bias[8] = {}, bias_u[8] = {};
+    if (a.bias && in) {
+        add8(bias, a.bias + c0);
+        if (kGated) add8(bias_u, a.bias + cols + c0);
+    }
+    static_for<NT>([&](auto t) {
+        uint4 res[kItems];
+#pragma unroll
+        for (int n = 0; n < kItems; n++) {
+            const int64_t tok = tw + 32 * t + n * (kWave / kOcts) + lane / kOcts;
+            res[n] = make_uint4(0, 0, 0, 0);
+            if (a.residual && in && tok < a.num_tokens) res[n] = residual8(a, tok, c0);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * Q; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                *reinterpret_cast<float4*>(&mine[c][32 * i + 8 * j + 4 * h]) =
+                    make_float4(acc[i][t][4 * j], acc[i][t][4 * j + 1], acc[i][t][4 * j + 2], acc[i][t][4 * j + 3]);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int n = 0; n < kItems; n++) {
+            const int row = n * (kWave / kOcts) + lane / kOcts;
+            float v[8], u[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = bias[i], u[i] = bias_u[i];
+            add8(v, &mine[row][kGated ? o / 4 * 64 + o % 4 * 8 : 8 * o]);
+            if (kGated) add8(u, &mine[row][o / 4 * 64 + 32 + o % 4 * 8]);
+            finish8(a, ACT, MX, cols, tw + 32 * t + row, c0, in && tw + 32 * t + row < a.num_tokens, v, u, res[n]);
         }
         __builtin_amdgcn_wave_barrier();
     });
@@ -423,6 +546,7 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
 // ------------------------------------------------------------ the choice
 constexpr int kRowsMaxTok = 128;   // tokens of linear_rows_kernel
 constexpr int kSplitMaxTok = 1024;  // most tokens whose inner axis is split
+constexpr int kMaxSplits = 8;
 
 struct LinearPlan {
     bool rows;       // linear_rows_kernel
@@ -430,6 +554,7 @@ struct LinearPlan {
     RowsGrid grid;
     bool wide;       // 256 x 256 tiles (else 128 x 128)
     TileGrid tile;
+    int splits;
 };
 
 LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation, bool mx) {
@@ -437,97 +562,96 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
     const int tiles = (int)((T + 15) / 16), chunks = (int)(inner / 128);
     const bool gated = activation == MOE_EPI_SILU_MUL;
     p.rows = T <= kRowsMaxTok;
+    int64_t splits = 1;
     if (!p.rows) {
         const int64_t wide_blocks = (rows + 255) / 256 * ((T + 255) / 256);
         p.wide = wide_blocks >= 192;
         const int n = p.wide ? 256 : 128;
         p.tile.row_blocks = (int)((rows + n - 1) / n);
         p.tile.tok_blocks = (int)((T + n - 1) / n);
-        int64_t splits = 1;
-        if (!p.wide && T <= kSplitMaxTok) {
-            splits = 512 / ((int64_t)p.tile.row_blocks * p.tile.tok_blocks);
-            if (splits > chunks / 8) splits = chunks / 8;
-            if (splits > 8 * T / (16 * tiles)) splits = 8 * T / (16 * tiles);
-        }
-        p.tile.splits = splits < 1 ? 1 : (int)splits;
-        p.tile.split_chunks = (chunks + p.tile.splits - 1) / p.tile.splits;
-        p.tile.splits = (chunks + p.tile.split_chunks - 1) / p.tile.split_chunks;
-        return p;
-    }
-    if (tiles <= 2) {
+        if (!p.wide && T <= kSplitMaxTok) splits = 512 / ((int64_t)p.tile.row_blocks * p.tile.tok_blocks);
+    } else if (tiles <= 2) {
         p.G = mx ? (gated ? 4 : 2) : gated ? 2 : 1;
         p.NT = tiles;
         p.W = 8;
         p.grid.groups = 1;
-        p.grid.splits = 1;
     } else {
         p.G = 4;
         p.W = 4;
         p.grid.groups = (tiles + 3) / 4;
         p.NT = (tiles + p.grid.groups - 1) / p.grid.groups;
-        // enough workgroups for two per CU, as long as each wave keeps two
-        // chunks and the partial sums stay within 32 bytes per product
-        int64_t splits = 512 / (rows / 64 * p.grid.groups);
-        if (splits > chunks / 8) splits = chunks / 8;
-        if (splits > 8 * T / (16 * tiles)) splits = 8 * T / (16 * tiles);
-        p.grid.splits = splits < 1 ? 1 : (int)splits;
+        splits = 512 / (rows / 64 * p.grid.groups);  // two workgroups per CU
     }
-    p.grid.units = (int)(rows / (16 * p.G));
-    p.grid.split_chunks = (chunks + p.grid.splits - 1) / p.grid.splits;
-    p.grid.splits = (chunks + p.grid.split_chunks - 1) / p.grid.split_chunks;
+    if (splits > chunks / 8) splits = chunks / 8;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    if (splits < 1) splits = 1;
+    const int per = (int)((chunks + splits - 1) / splits);
+    p.splits = (chunks + per - 1) / per;
+    p.grid.splits = p.tile.splits = p.splits;
+    p.grid.split_chunks = p.tile.split_chunks = per;
+    if (p.rows) p.grid.units = (int)(rows / (16 * p.G));
     return p;
 }
 
 template <int G, int NT, int W>
-void launch_rows(const moe_mxfp8_linear_args& a, const RowsGrid& p, hipStream_t stream) {
+hipError_t launch_rows(const moe_mxfp8_linear_args& a, const RowsGrid& p, hipStream_t stream) {
     const unsigned grid = (unsigned)(p.splits * 8 * p.groups * ((p.units + 7) / 8));
     linear_rows_kernel<G, NT, W><<<grid, W * kWave, 0, stream>>>(a, p);
+    return hipGetLastError();
 }
 
-template <int RQ, int TT, int WR, int WT>
+template <int ACT, bool MX, int RQ, int TT, int WR, int WT>
 hipError_t launch_tile(const moe_mxfp8_linear_args& a, const TileGrid& p, hipStream_t stream) {
-    constexpr int bytes = sizeof(TileSmem<RQ, TT, 2>);
-    const auto kernel = linear_tile_kernel<RQ, TT, WR, WT>;
-    if (bytes > 65536) {  // more than 64 KB of LDS has to be asked for
-        const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                   hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (err != hipSuccess) return err;
-    }
+    constexpr int bytes = sizeof(TileSmem<RQ, TT, 2>);  // more than 64 KB: has to be asked for
+    const auto kernel = linear_tile_kernel<ACT, MX, RQ, TT, WR, WT>;
+    const hipError_t err =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err != hipSuccess) return err;
     const unsigned grid = (unsigned)((int64_t)p.splits * p.row_blocks * p.tok_blocks);
     kernel<<<grid, WR * WT * kWave, bytes, stream>>>(a, p);
     return hipGetLastError();
 }
 
-int splits_of(const LinearPlan& p) { return p.rows ? p.grid.splits : p.tile.splits; }
+template <int ACT, bool MX>
+hipError_t launch_tiles(const moe_mxfp8_linear_args& a, const LinearPlan& p, hipStream_t stream) {
+    return p.wide ? launch_tile<ACT, MX, 4, 8, 2, 4>(a, p.tile, stream)
+                  : launch_tile<ACT, MX, 2, 4, 2, 2>(a, p.tile, stream);
+}
 
 }  // namespace
 
 int64_t mxfp8_linear_workspace(int64_t T, int64_t rows, int64_t inner, int32_t activation) {
     if (T == 0) return 0;
-    const int splits = splits_of(make_plan(T, rows, inner, activation, false));
-    return splits > 1 ? splits * ((T + 15) / 16) * rows * 64 : 0;
+    const int splits = make_plan(T, rows, inner, activation, false).splits;
+    return splits > 1 ? splits * T * rows * 4 : 0;
 }
 
 hipError_t launch_mxfp8_linear(const moe_mxfp8_linear_args& a, hipStream_t stream) {
-    const LinearPlan p = make_plan(a.num_tokens, a.rows, a.inner, a.activation, a.out_codes != nullptr);
+    const bool mx = a.out_codes != nullptr;
+    const LinearPlan p = make_plan(a.num_tokens, a.rows, a.inner, a.activation, mx);
     const RowsGrid& r = p.grid;
-    hipError_t err = hipSuccess;
+    hipError_t err;
     if (!p.rows) {
-        err = p.wide ? launch_tile<4, 16, 2, 4>(a, p.tile, stream) : launch_tile<2, 8, 2, 2>(a, p.tile, stream);
+        switch (p.splits > 1 ? MOE_EPI_NONE : a.activation) {  // a split leaves the epilogue to the finishing kernel
+            case MOE_EPI_SILU: err = mx ? launch_tiles<MOE_EPI_SILU, true>(a, p, stream)
+                                        : launch_tiles<MOE_EPI_SILU, false>(a, p, stream); break;
+            case MOE_EPI_GELU: err = mx ? launch_tiles<MOE_EPI_GELU, true>(a, p, stream)
+                                        : launch_tiles<MOE_EPI_GELU, false>(a, p, stream); break;
+            case MOE_EPI_SILU_MUL: err = mx ? launch_tiles<MOE_EPI_SILU_MUL, true>(a, p, stream)
+                                            : launch_tiles<MOE_EPI_SILU_MUL, false>(a, p, stream); break;
+            default: err = mx && p.splits == 1 ? launch_tiles<MOE_EPI_NONE, true>(a, p, stream)
+                                               : launch_tiles<MOE_EPI_NONE, false>(a, p, stream); break;
+        }
     } else if (p.W == 8) {
-        if (p.G == 1) p.NT == 1 ? launch_rows<1, 1, 8>(a, r, stream) : launch_rows<1, 2, 8>(a, r, stream);
-        else if (p.G == 2) p.NT == 1 ? launch_rows<2, 1, 8>(a, r, stream) : launch_rows<2, 2, 8>(a, r, stream);
-        else p.NT == 1 ? launch_rows<4, 1, 8>(a, r, stream) : launch_rows<4, 2, 8>(a, r, stream);
-        err = hipGetLastError();
+        if (p.G == 1) err = p.NT == 1 ? launch_rows<1, 1, 8>(a, r, stream) : launch_rows<1, 2, 8>(a, r, stream);
+        else if (p.G == 2) err = p.NT == 1 ? launch_rows<2, 1, 8>(a, r, stream) : launch_rows<2, 2, 8>(a, r, stream);
+        else err = p.NT == 1 ? launch_rows<4, 1, 8>(a, r, stream) : launch_rows<4, 2, 8>(a, r, stream);
     } else {
-        if (p.NT <= 3) launch_rows<4, 3, 4>(a, r, stream);
-        else launch_rows<4, 4, 4>(a, r, stream);
-        err = hipGetLastError();
+        err = p.NT <= 3 ? launch_rows<4, 3, 4>(a, r, stream) : launch_rows<4, 4, 4>(a, r, stream);
     }
-    const int splits = splits_of(p);
-    if (err != hipSuccess || splits == 1) return err;
-    const int64_t units = a.rows / 64 * ((a.num_tokens + 15) / 16);
-    linear_finish_kernel<<<(unsigned)((units + 3) / 4), 256, 0, stream>>>(a, splits);
+    if (err != hipSuccess || p.splits == 1) return err;
+    const int64_t octs = a.num_tokens * (a.activation == MOE_EPI_SILU_MUL ? a.rows / 2 : a.rows) / 8;
+    linear_finish_kernel<<<(unsigned)((octs + 255) / 256), 256, 0, stream>>>(a, p.splits);
     return hipGetLastError();
 }
 
