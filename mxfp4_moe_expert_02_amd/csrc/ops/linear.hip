@@ -19,6 +19,9 @@
 #include "lds_dma.h"
 #include "ops_internal.h"
 
+#ifndef WTT
+#define WTT 2
+#endif
 namespace moe {
 namespace {
 
@@ -358,7 +361,8 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
     constexpr int kStages = 2, kWaves = WR * WT;
     constexpr int Q = RQ / WR, NT = TT / WT;                   // a wave's quads and token tiles
     constexpr int kA = RQ * 8 / kWaves, kB = TT * 4 / kWaves;  // 1 KB loads per wave and chunk
-    static_assert(RQ * 8 % kWaves == 0 && TT * 4 % kWaves == 0 && RQ + TT / 2 == kWaves, "loads per wave");
+    constexpr int kS = (RQ + TT / 2) / kWaves;                 // and 256-byte loads of block scales
+    static_assert(RQ * 8 % kWaves == 0 && TT * 4 % kWaves == 0 && (RQ + TT / 2) % kWaves == 0, "loads per wave");
     extern __shared__ uint8_t smem_raw[];
     auto& sm = *reinterpret_cast<TileSmem<RQ, TT, kStages>*>(smem_raw);
     const int w = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, c = lane % 32, h = lane / 32;
@@ -387,24 +391,27 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
         offB[i] = (uint32_t)min(row, last) * (uint32_t)a.inner + ((lane % 8) ^ (row / 2 % 8)) * 16;
     }
     const uint8_t* baseB = a.x_codes + t0 * a.inner + (int64_t)k0 * 128;
-    const uint8_t* baseS;
-    uint32_t offS;
-    int step_s;
-    if (w < RQ) {
-        baseS = a.w_scales + ((int64_t)min(q0 + w, quads - 1) * chunks + k0) * 256;
-        offS = lane * 4;
-        step_s = 256;
-    } else {
-        baseS = a.x_scales + t0 * (a.inner / 32) + (int64_t)k0 * 4;
-        offS = (uint32_t)min((w - RQ) * kWave + lane, last) * (uint32_t)(a.inner / 32);
-        step_s = 4;
+    const uint8_t* baseS[kS];
+    uint32_t offS[kS];
+    int step_s[kS];
+#pragma unroll
+    for (int i = 0; i < kS; i++) {
+        const int n = w * kS + i;
+        if (n < RQ) {
+            baseS[i] = a.w_scales + ((int64_t)min(q0 + n, quads - 1) * chunks + k0) * 256;
+            offS[i] = lane * 4;
+            step_s[i] = 256;
+        } else {
+            baseS[i] = a.x_scales + t0 * (a.inner / 32) + (int64_t)k0 * 4;
+            offS[i] = (uint32_t)min((n - RQ) * kWave + lane, last) * (uint32_t)(a.inner / 32);
+            step_s[i] = 4;
+        }
     }
     const uint32_t lds = lds_addr(smem_raw);
     constexpr uint32_t kBufA = RQ * 8192, kBufB = TT * 4096, kBufS = (RQ * kWave + TT * 32) * 4;
     constexpr uint32_t kAtB = kStages * kBufA, kAtS = kAtB + kStages * kBufB;
-    const uint32_t ldsS = lds + kAtS + w * (kWave * 4);
     // load n of the kLoads of this wave's next chunk, into buffer buf
-    constexpr int kLoads = kA + kB + 1;
+    constexpr int kLoads = kA + kB + kS;
     auto issue = [&](auto n, int buf) {
         constexpr int i = decltype(n)::value;
         if constexpr (i < kB) {
@@ -414,8 +421,9 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
             dma16s(baseA[i - kB], lane * 16, lds + buf * kBufA + (w * kA + i - kB) * 1024);
             baseA[i - kB] += 8192;
         } else {
-            dma4s(baseS, offS, ldsS + buf * kBufS);
-            baseS += step_s;
+            constexpr int j = i - kB - kA;
+            dma4s(baseS[j], offS[j], lds + kAtS + buf * kBufS + (w * kS + j) * (kWave * 4));
+            baseS[j] += step_s[j];
         }
     };
     const int wr = w % WR, wt = w / WR;
@@ -424,53 +432,82 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
     for (int i = 0; i < 2 * Q; i++)
 #pragma unroll
         for (int t = 0; t < NT; t++) acc[i][t] = f32x16_t{};
-    static_for<kLoads>([&](auto n) { issue(n, 0); });
-    int buf = 0;
     // A: row r of 32 is row r % 16 of group r / 16; piece 4s + h (then + 2) is
     // half h, lane r % 16 + 32 s (then + 16).  Its scale byte is that of the
     // group: the odd group's is shifted down to the even one's place.
     const int r = c % 16, a_at = c / 16 * 2048 + h * 1024 + r * 16, as_at = r + 16 * h, as_shift = c / 16 * 8;
     const int b_at = c * 128 + (h ^ (c / 2 % 8)) * 16;
-    auto step = [&](auto more) {
-        // this wave's loads of the chunk have landed; after the barrier every
-        // wave's have, and every wave has what it read of the other buffer
+    struct Operands {
+        i32x8_t A[2 * Q], B[NT];
+        uint32_t sa[Q], sb[NT];
+    } o0, o1;  // of the two products of a chunk
+    // one operand (B tiles first, then A tiles) of product s of the chunk in `buf`
+    constexpr int kUnits = NT + 2 * Q;
+    auto read = [&](Operands& o, int buf, auto s, auto n) {
+        constexpr int u = decltype(n)::value;
+        if constexpr (u < NT) {
+            const uint8_t* row = sm.b[buf][wt * NT + u];
+            o.B[u] = operand(*reinterpret_cast<const uint4*>(row + (b_at ^ (64 * s))),
+                             *reinterpret_cast<const uint4*>(row + (b_at ^ (64 * s + 32))));
+            o.sb[u] = sm.s[buf].b[(wt * NT + u) * 32 + c] >> (8 * h);
+        } else {
+            constexpr int q = (u - NT) / 2, i = (u - NT) % 2;
+            const uint8_t* qa = &sm.a[buf][wr * Q + q][a_at + 512 * s + i * 4096];
+            if (i == 0) o.sa[q] = sm.s[buf].a[wr * Q + q][as_at + 32 * s] >> as_shift;
+            o.A[u - NT] = operand(*reinterpret_cast<const uint4*>(qa), *reinterpret_cast<const uint4*>(qa + 256));
+        }
+    };
+    // the products of one operand set; after the n-th of them also(n) goes
+    // out, and the compiler keeps that order
+    constexpr int kMfma = 2 * Q * NT;
+    auto multiply = [&](const Operands& o, auto s, auto&& also) {
+        static_for<kMfma>([&](auto n) {
+            constexpr int i = decltype(n)::value / NT, t = decltype(n)::value % NT;
+            acc[i][t] = mfma32<2 * (i % 2), 2 * decltype(s)::value>(o.A[i], o.B[t], acc[i][t], o.sa[i / 2], o.sb[t]);
+            also(n);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    // part n of kMfma of something done in `count` steps
+    auto spread = [&](auto n, auto count, auto&& f) {
+        constexpr int lo = decltype(n)::value * decltype(count)::value / kMfma;
+        constexpr int hi = (decltype(n)::value + 1) * decltype(count)::value / kMfma;
+        static_for<hi - lo>([&](auto j) { f(std::integral_constant<int, lo + decltype(j)::value>{}); });
+    };
+    const std::integral_constant<int, kUnits> units;
+    const std::integral_constant<int, kLoads> loads;
+    // Operands are read half a chunk ahead: the first product's while the
+    // second of the chunk before runs.  In the middle of a chunk this wave
+    // has read all of it (lgkmcnt) and its loads of the next have landed
+    // (vmcnt); after the barrier that holds for every wave, so the next
+    // chunk can be read and the one after it loaded over this one.
+    const std::integral_constant<int, 0> s0;
+    const std::integral_constant<int, 1> s1;
+    static_for<kLoads>([&](auto n) { issue(n, 0); });
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    if (k0 + 1 < k1) static_for<kLoads>([&](auto n) { issue(n, 1); });
+    static_for<kUnits>([&](auto n) { read(o0, 0, s0, n); });
+    int buf = 0;
+    auto first_half = [&] {
+        multiply(o0, s0, [&](auto n) { spread(n, units, [&](auto u) { read(o1, buf, s1, u); }); });
+    };
+    for (int k = k0; k + 2 < k1; k++) {
+        first_half();
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        uint32_t sb[NT];
-#pragma unroll
-        for (int t = 0; t < NT; t++) sb[t] = sm.s[buf].b[(wt * NT + t) * 32 + c] >> (8 * h);
-        static_for<2>([&](auto s) {
-            i32x8_t B[NT];
-#pragma unroll
-            for (int t = 0; t < NT; t++) {
-                const uint8_t* row = sm.b[buf][wt * NT + t];
-                B[t] = operand(*reinterpret_cast<const uint4*>(row + (b_at ^ (64 * s))),
-                               *reinterpret_cast<const uint4*>(row + (b_at ^ (64 * s + 32))));
-            }
-            static_for<Q>([&](auto q) {
-                const uint8_t* qa = &sm.a[buf][wr * Q + q][a_at + 512 * s];
-                const uint32_t sa = sm.s[buf].a[wr * Q + q][as_at + 32 * s] >> as_shift;
-                static_for<2>([&](auto i) {
-                    const i32x8_t A = operand(*reinterpret_cast<const uint4*>(qa + i * 4096),
-                                              *reinterpret_cast<const uint4*>(qa + i * 4096 + 256));
-#pragma unroll
-                    for (int t = 0; t < NT; t++)
-                        acc[2 * q + i][t] = mfma32<2 * decltype(i)::value, 2 * decltype(s)::value>(
-                            A, B[t], acc[2 * q + i][t], sa, sb[t]);
-                    // the next chunk's loads go out between the products
-                    constexpr int at = (decltype(s)::value * Q + decltype(q)::value) * 2 + decltype(i)::value;
-                    constexpr int per = (kLoads + 4 * Q - 1) / (4 * Q);
-                    if constexpr (decltype(more)::value)
-                        static_for<per>([&](auto j) {
-                            constexpr int n = at * per + decltype(j)::value;
-                            if constexpr (n < kLoads) issue(std::integral_constant<int, n>{}, buf ^ 1);
-                        });
-                });
-            });
+        multiply(o1, s1, [&](auto n) {
+            spread(n, units, [&](auto u) { read(o0, buf ^ 1, s0, u); });
+            spread(n, loads, [&](auto u) { issue(u, buf); });
         });
         buf ^= 1;
-    };
-    for (int k = k0; k + 1 < k1; k++) step(std::true_type{});
-    step(std::false_type{});
+    }
+    if (k0 + 1 < k1) {  // the last but one: nothing more to load
+        first_half();
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        multiply(o1, s1, [&](auto n) { spread(n, units, [&](auto u) { read(o0, buf ^ 1, s0, u); }); });
+        buf ^= 1;
+    }
+    first_half();
+    multiply(o1, s1, [](auto) {});
 
     // The sums go through this wave's own part of the LDS, one token tile at
     // a time, to lanes that hold 8 consecutive columns of a token: rows of 16
@@ -614,7 +651,7 @@ hipError_t launch_tile(const moe_mxfp8_linear_args& a, const TileGrid& p, hipStr
 
 template <int ACT, bool MX>
 hipError_t launch_tiles(const moe_mxfp8_linear_args& a, const LinearPlan& p, hipStream_t stream) {
-    return p.wide ? launch_tile<ACT, MX, 4, 8, 2, 4>(a, p.tile, stream)
+    return p.wide ? launch_tile<ACT, MX, 4, 8, 2, WTT>(a, p.tile, stream)
                   : launch_tile<ACT, MX, 2, 4, 2, 2>(a, p.tile, stream);
 }
 
