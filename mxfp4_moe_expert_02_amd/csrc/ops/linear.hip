@@ -19,6 +19,9 @@
 #include "lds_dma.h"
 #include "ops_internal.h"
 
+#ifndef ROWS_D
+#define ROWS_D 2
+#endif
 namespace moe {
 namespace {
 
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(moe_mxfp8_linear_arg
 // go from global memory to registers (a tile-layout load is a contiguous 1 KB
 // per wave), token rows through the wave's own LDS, as whole 128-byte lines
 // (16 rows x 16 bytes per quarter wave, which the operand order would give,
-// cost a cache access per lane); both two chunks ahead.
+// cost a cache access per lane); both D chunks ahead.
 constexpr int kSegment = 16;  // chunks whose token scales a wave holds in LDS
 
 struct RowsGrid {
@@ -162,16 +165,16 @@ struct RowsGrid {
     int splits, split_chunks;   // parts of the inner axis, chunks of one
 };
 
-template <int NT>
+template <int NT, int D>
 struct RowsWave {  // one wave's staged tokens
-    alignas(16) uint8_t x[2][NT][16 * 128];            // rows of 128 bytes, piece p of row c in slot p ^ (c / 2 % 8)
+    alignas(16) uint8_t x[D][NT][16 * 128];            // rows of 128 bytes, piece p of row c in slot p ^ (c / 2 % 8)
     alignas(16) uint8_t s[NT][kSegment / 4][16 * 16];  // scale bytes [row][4 chunks][4 blocks]
 };
 
-template <int G, int NT, int W>
+template <int G, int NT, int W, int D>
 __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear_args a, RowsGrid p) {
     union Smem {
-        RowsWave<NT> wave[W];
+        RowsWave<NT, D> wave[W];
         float sum[W][NT * 16][16 * G + 4];  // [wave][token][row], padded
     };
     __shared__ Smem sm;
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear
         }
         xs[t] = a.x_scales + (t0 + min(16 * t + lane / 4, last)) * (a.inner / 32);
     }
-    RowsWave<NT>& mine = sm.wave[w];
+    RowsWave<NT, D>& mine = sm.wave[w];
     f32x4_t acc[NT][G];
 #pragma unroll
     for (int t = 0; t < NT; t++)
@@ -214,10 +217,8 @@ __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear
     struct Weights {
         u32x4_t v[G][2];
         uint32_t s;
-    } wb[2];
-    // chunk k (one past the run repeats its last one and is not used)
-    auto load = [&](Weights& r, int k, int buf) {
-        const int ch = min(k, r1 - 1);
+    } wb[D];
+    auto load = [&](Weights& r, int ch, int buf) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what was read of this buffer has arrived
 #pragma unroll
         for (int t = 0; t < NT; t++)
@@ -266,17 +267,25 @@ __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear
 #pragma unroll
             for (int t = 0; t < NT; t++)
                 dma4(xs[t] + min(seg + 4 * j + lane % 4, r1 - 1) * 4, lds_addr(&mine.s[t][j][0]));
-        load(wb[0], seg, 0);
-        load(wb[1], seg + 1, 1);
-        for (int i = 0; i < n; i += 2) {
-            // the wave's own loads of chunk i have landed (those of i + 1 may be in flight)
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
-            multiply(wb[0], i, 0);
-            load(wb[0], seg + i + 2, 0);
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
-            if (i + 1 < n) multiply(wb[1], i + 1, 1);
-            load(wb[1], seg + i + 3, 1);
-        }
+        static_for<D>([&](auto d) {
+            if (d < n) load(wb[d], seg + d, d);
+        });
+        // In the steady loop every load is unconditional (a skipped one makes
+        // the compiler wait for all); the last chunks have none to skip.
+        int i = 0;
+        for (; i + 2 * D <= n; i += D)
+            static_for<D>([&](auto d) {
+                // this chunk has landed, the next D - 1 may be in flight
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * kLoads) : "memory");
+                multiply(wb[d], i + d, d);
+                load(wb[d], seg + i + D + d, d);
+            });
+        static_for<2 * D - 1>([&](auto d) {
+            if (i + d >= n) return;
+            if (d == 0 || d == D) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            multiply(wb[d % D], i + d, d % D);
+            if (i + D + d < n) load(wb[d % D], seg + i + D + d, d % D);
+        });
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
     __syncthreads();
@@ -348,14 +357,21 @@ struct TileGrid {
     int splits, split_chunks;
 };
 
+// this wave's loads but the newest N have landed and its LDS reads arrived;
+// past the barrier, every wave's
+template <int N>
+__device__ inline void wait_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 template <int SA, int SB>
 __device__ inline f32x16_t mfma32(const i32x8_t& A, const i32x8_t& B, const f32x16_t& c, uint32_t sa, uint32_t sb) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 0, 0, SA, (int)sa, SB, (int)sb);
 }
 
-template <int ACT, bool MX, int RQ, int TT, int WR, int WT>
+template <int ACT, bool MX, int RQ, int TT, int WR, int WT, int STAGES>
 __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_linear_args a, TileGrid p) {
-    constexpr int kStages = 2, kWaves = WR * WT;
+    constexpr int kStages = STAGES, kWaves = WR * WT;
     constexpr int Q = RQ / WR, NT = TT / WT;                   // a wave's quads and token tiles
     constexpr int kA = RQ * 8 / kWaves, kB = TT * 4 / kWaves;  // 1 KB loads per wave and chunk
     constexpr int kS = (RQ + TT / 2) / kWaves;                 // and 256-byte loads of block scales
@@ -486,31 +502,37 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
     // second of the chunk before runs.  In the middle of a chunk this wave
     // has read all of it (lgkmcnt) and its loads of the next have landed
     // (vmcnt); after the barrier that holds for every wave, so the next
-    // chunk can be read and the one after it loaded over this one.
+    // chunk can be read and the one kStages on loaded over this one.
     const std::integral_constant<int, 0> s0;
     const std::integral_constant<int, 1> s1;
-    static_for<kLoads>([&](auto n) { issue(n, 0); });
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    if (k0 + 1 < k1) static_for<kLoads>([&](auto n) { issue(n, 1); });
+    const int n_chunks = k1 - k0;
+    static_for<kStages>([&](auto st) {
+        if (st < n_chunks) static_for<kLoads>([&](auto n) { issue(n, st); });
+    });
+    // the first chunk's loads have landed (those of the others may be in flight)
+    if (n_chunks >= kStages) wait_barrier<(kStages - 1) * kLoads>();
+    else wait_barrier<0>();
     static_for<kUnits>([&](auto n) { read(o0, 0, s0, n); });
     int buf = 0;
+    auto next = [&] { return buf + 1 == kStages ? 0 : buf + 1; };
     auto first_half = [&] {
         multiply(o0, s0, [&](auto n) { spread(n, units, [&](auto u) { read(o1, buf, s1, u); }); });
     };
-    for (int k = k0; k + 2 < k1; k++) {
+    int k = 0;
+    for (; k + kStages < n_chunks; k++) {
         first_half();
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        wait_barrier<(kStages - 2) * kLoads>();
         multiply(o1, s1, [&](auto n) {
-            spread(n, units, [&](auto u) { read(o0, buf ^ 1, s0, u); });
+            spread(n, units, [&](auto u) { read(o0, next(), s0, u); });
             spread(n, loads, [&](auto u) { issue(u, buf); });
         });
-        buf ^= 1;
+        buf = next();
     }
-    if (k0 + 1 < k1) {  // the last but one: nothing more to load
+    for (; k + 1 < n_chunks; k++) {  // nothing more to load
         first_half();
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        multiply(o1, s1, [&](auto n) { spread(n, units, [&](auto u) { read(o0, buf ^ 1, s0, u); }); });
-        buf ^= 1;
+        wait_barrier<0>();
+        multiply(o1, s1, [&](auto n) { spread(n, units, [&](auto u) { read(o0, next(), s0, u); }); });
+        buf = next();
     }
     first_half();
     multiply(o1, s1, [](auto) {});
@@ -596,6 +618,7 @@ struct LinearPlan {
     int G, NT, W;
     RowsGrid grid;
     bool wide;       // 256 x 256 tiles (else 128 x 128)
+    bool deep;       // 128 x 128 tiles staged three chunks deep (else two)
     TileGrid tile;
     int splits;
 };
@@ -612,7 +635,7 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
         const int n = p.wide ? 256 : 128;
         p.tile.row_blocks = (int)((rows + n - 1) / n);
         p.tile.tok_blocks = (int)((T + n - 1) / n);
-        if (!p.wide && T <= kSplitMaxTok) splits = 512 / ((int64_t)p.tile.row_blocks * p.tile.tok_blocks);
+        if (!p.wide && T <= kSplitMaxTok) splits = 256 / ((int64_t)p.tile.row_blocks * p.tile.tok_blocks);
     } else if (tiles <= 2) {
         p.G = mx ? (gated ? 4 : 2) : gated ? 2 : 1;
         p.NT = tiles;
@@ -628,6 +651,12 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
     if (splits > chunks / 8) splits = chunks / 8;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;
+    // 128 x 128 tiles: up to one workgroup per CU the loads of two chunks
+    // are kept in flight (three stages, 101 KB of LDS); beyond that two
+    // workgroups per CU hide each other's waits (two stages).  512 x 4096 x
+    // 7168: 256 workgroups 31.6 us deep, 34.4 otherwise; 1024 x 7168 x 7168:
+    // 448 workgroups 76.7 deep, 66.3 otherwise.
+    p.deep = !p.rows && !p.wide && (int64_t)p.tile.row_blocks * p.tile.tok_blocks * splits <= 256;
     const int per = (int)((chunks + splits - 1) / splits);
     p.splits = (chunks + per - 1) / per;
     p.grid.splits = p.tile.splits = p.splits;
@@ -636,17 +665,17 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
     return p;
 }
 
-template <int G, int NT, int W>
+template <int G, int NT, int W, int D = ROWS_D>
 hipError_t launch_rows(const moe_mxfp8_linear_args& a, const RowsGrid& p, hipStream_t stream) {
     const unsigned grid = (unsigned)(p.splits * 8 * p.groups * ((p.units + 7) / 8));
-    linear_rows_kernel<G, NT, W><<<grid, W * kWave, 0, stream>>>(a, p);
+    linear_rows_kernel<G, NT, W, D><<<grid, W * kWave, 0, stream>>>(a, p);
     return hipGetLastError();
 }
 
-template <int ACT, bool MX, int RQ, int TT, int WR, int WT>
+template <int ACT, bool MX, int RQ, int TT, int WR, int WT, int STAGES>
 hipError_t launch_tile(const moe_mxfp8_linear_args& a, const TileGrid& p, hipStream_t stream) {
-    constexpr int bytes = sizeof(TileSmem<RQ, TT, 2>);  // more than 64 KB: has to be asked for
-    const auto kernel = linear_tile_kernel<ACT, MX, RQ, TT, WR, WT>;
+    constexpr int bytes = sizeof(TileSmem<RQ, TT, STAGES>);  // more than 64 KB: has to be asked for
+    const auto kernel = linear_tile_kernel<ACT, MX, RQ, TT, WR, WT, STAGES>;
     const hipError_t err =
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != hipSuccess) return err;
@@ -657,8 +686,9 @@ hipError_t launch_tile(const moe_mxfp8_linear_args& a, const TileGrid& p, hipStr
 
 template <int ACT, bool MX>
 hipError_t launch_tiles(const moe_mxfp8_linear_args& a, const LinearPlan& p, hipStream_t stream) {
-    return p.wide ? launch_tile<ACT, MX, 4, 8, 2, 4>(a, p.tile, stream)
-                  : launch_tile<ACT, MX, 2, 4, 2, 2>(a, p.tile, stream);
+    if (p.wide) return launch_tile<ACT, MX, 4, 8, 2, 4, 2>(a, p.tile, stream);
+    return p.deep ? launch_tile<ACT, MX, 2, 4, 2, 2, 3>(a, p.tile, stream)
+                  : launch_tile<ACT, MX, 2, 4, 2, 2, 2>(a, p.tile, stream);
 }
 
 }  // namespace
