@@ -19,9 +19,6 @@
 #include "lds_dma.h"
 #include "ops_internal.h"
 
-#ifndef ROWS_D
-#define ROWS_D 2
-#endif
 namespace moe {
 namespace {
 
@@ -612,6 +609,7 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
 constexpr int kRowsMaxTok = 128;   // tokens of linear_rows_kernel
 constexpr int kSplitMaxTok = 1024;  // most tokens whose inner axis is split
 constexpr int kMaxSplits = 8;
+constexpr int kCus = 256;
 
 struct LinearPlan {
     bool rows;       // linear_rows_kernel
@@ -635,18 +633,32 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
         const int n = p.wide ? 256 : 128;
         p.tile.row_blocks = (int)((rows + n - 1) / n);
         p.tile.tok_blocks = (int)((T + n - 1) / n);
-        if (!p.wide && T <= kSplitMaxTok) splits = 256 / ((int64_t)p.tile.row_blocks * p.tile.tok_blocks);
-    } else if (tiles <= 2) {
-        p.G = mx ? (gated ? 4 : 2) : gated ? 2 : 1;
-        p.NT = tiles;
-        p.W = 8;
-        p.grid.groups = 1;
+        if (!p.wide && T <= kSplitMaxTok) splits = kCus / ((int64_t)p.tile.row_blocks * p.tile.tok_blocks);
     } else {
-        p.G = 4;
-        p.W = 4;
-        p.grid.groups = (tiles + 3) / 4;
-        p.NT = (tiles + p.grid.groups - 1) / p.grid.groups;
-        splits = 512 / (rows / 64 * p.grid.groups);  // two workgroups per CU
+        // Of the tile shapes, the one whose workgroups come closest to one
+        // per CU from below: fewer leave CUs idle, more take a second round
+        // (and read the tokens or the weights more often).  Measured on 30
+        // shapes of 9 to 128 tokens; e.g. 24 x 7168 x 7168: 224 workgroups
+        // 15.3 us, 448 17.6, 112 19.3; 96 x 4096 x 7168: 256 15.1, 192 16.4,
+        // 384 18.9.  Equal counts: the smaller tile.
+        int64_t best = 0;
+        for (int G = mx && gated ? 4 : mx || gated ? 2 : 1; G <= 4; G *= 2)
+            for (int NT = 1; NT <= 4; NT++) {
+                if (NT > tiles || (NT == 4 && G == 1)) continue;
+                const int64_t n = rows / (16 * G) * ((tiles + NT - 1) / NT);
+                const bool fits = n <= kCus, best_fits = best <= kCus;
+                if (best && (fits != best_fits ? best_fits : fits ? n < best : n > best)) continue;
+                if (best == n && G * NT >= p.G * p.NT) continue;
+                best = n;
+                p.G = G;
+                p.NT = NT;
+            }
+        p.W = p.NT == 4 ? 4 : 8;  // what the staged tokens leave room for
+        p.grid.groups = (tiles + p.NT - 1) / p.NT;
+        // MXFP8 output needs whole blocks of columns in a workgroup; where
+        // that leaves few of them the inner axis is split (9 x 4096 x 6144
+        // gated: 64 workgroups 13.2 us, 4 times as many 11.1)
+        if (mx && best <= kCus / 4) splits = 4;
     }
     if (splits > chunks / 8) splits = chunks / 8;
     if (splits > kMaxSplits) splits = kMaxSplits;
@@ -656,7 +668,7 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
     // workgroups per CU hide each other's waits (two stages).  512 x 4096 x
     // 7168: 256 workgroups 31.6 us deep, 34.4 otherwise; 1024 x 7168 x 7168:
     // 448 workgroups 76.7 deep, 66.3 otherwise.
-    p.deep = !p.rows && !p.wide && (int64_t)p.tile.row_blocks * p.tile.tok_blocks * splits <= 256;
+    p.deep = !p.rows && !p.wide && (int64_t)p.tile.row_blocks * p.tile.tok_blocks * splits <= kCus;
     const int per = (int)((chunks + splits - 1) / splits);
     p.splits = (chunks + per - 1) / per;
     p.grid.splits = p.tile.splits = p.splits;
@@ -665,10 +677,10 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
     return p;
 }
 
-template <int G, int NT, int W, int D = ROWS_D>
+template <int G, int NT, int W>
 hipError_t launch_rows(const moe_mxfp8_linear_args& a, const RowsGrid& p, hipStream_t stream) {
     const unsigned grid = (unsigned)(p.splits * 8 * p.groups * ((p.units + 7) / 8));
-    linear_rows_kernel<G, NT, W, D><<<grid, W * kWave, 0, stream>>>(a, p);
+    linear_rows_kernel<G, NT, W, 2><<<grid, W * kWave, 0, stream>>>(a, p);
     return hipGetLastError();
 }
 
@@ -695,7 +707,8 @@ hipError_t launch_tiles(const moe_mxfp8_linear_args& a, const LinearPlan& p, hip
 
 int64_t mxfp8_linear_workspace(int64_t T, int64_t rows, int64_t inner, int32_t activation) {
     if (T == 0) return 0;
-    const int splits = make_plan(T, rows, inner, activation, false).splits;
+    // either output may be asked for: MXFP8 splits wherever bf16 does
+    const int splits = make_plan(T, rows, inner, activation, true).splits;
     return splits > 1 ? splits * T * rows * 4 : 0;
 }
 
@@ -715,12 +728,20 @@ hipError_t launch_mxfp8_linear(const moe_mxfp8_linear_args& a, hipStream_t strea
             default: err = mx && p.splits == 1 ? launch_tiles<MOE_EPI_NONE, true>(a, p, stream)
                                                : launch_tiles<MOE_EPI_NONE, false>(a, p, stream); break;
         }
-    } else if (p.W == 8) {
-        if (p.G == 1) err = p.NT == 1 ? launch_rows<1, 1, 8>(a, r, stream) : launch_rows<1, 2, 8>(a, r, stream);
-        else if (p.G == 2) err = p.NT == 1 ? launch_rows<2, 1, 8>(a, r, stream) : launch_rows<2, 2, 8>(a, r, stream);
-        else err = p.NT == 1 ? launch_rows<4, 1, 8>(a, r, stream) : launch_rows<4, 2, 8>(a, r, stream);
     } else {
-        err = p.NT <= 3 ? launch_rows<4, 3, 4>(a, r, stream) : launch_rows<4, 4, 4>(a, r, stream);
+        switch (p.G * 10 + p.NT) {
+            case 11: err = launch_rows<1, 1, 8>(a, r, stream); break;
+            case 12: err = launch_rows<1, 2, 8>(a, r, stream); break;
+            case 13: err = launch_rows<1, 3, 8>(a, r, stream); break;
+            case 21: err = launch_rows<2, 1, 8>(a, r, stream); break;
+            case 22: err = launch_rows<2, 2, 8>(a, r, stream); break;
+            case 23: err = launch_rows<2, 3, 8>(a, r, stream); break;
+            case 24: err = launch_rows<2, 4, 4>(a, r, stream); break;
+            case 41: err = launch_rows<4, 1, 8>(a, r, stream); break;
+            case 42: err = launch_rows<4, 2, 8>(a, r, stream); break;
+            case 43: err = launch_rows<4, 3, 8>(a, r, stream); break;
+            default: err = launch_rows<4, 4, 4>(a, r, stream); break;
+        }
     }
     if (err != hipSuccess || p.splits == 1) return err;
     const int64_t octs = a.num_tokens * (a.activation == MOE_EPI_SILU_MUL ? a.rows / 2 : a.rows) / 8;
