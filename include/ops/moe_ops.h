@@ -84,7 +84,7 @@ typedef struct moe_rmsnorm_args {
     int64_t y_stride;
     uint8_t* codes;           /* [num_tokens, hidden] E4M3, contiguous rows; NULL together with scales */
     uint8_t* scales;          /* [num_tokens, hidden / 32] E8M0, contiguous */
-    int64_t num_tokens;       /* 0 .. 2^22 */
+    int64_t num_tokens;       /* 0 .. 2^20 */
     int64_t hidden;           /* a multiple of 32, 32 .. 16384 */
 } moe_rmsnorm_args;
 

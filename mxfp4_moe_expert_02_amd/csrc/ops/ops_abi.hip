@@ -24,7 +24,7 @@ int done(hipError_t err, const char* what) { return err == hipSuccess ? MOE_OK :
 constexpr int64_t kMaxSlots = 1ll << 25;
 
 int check_norm(moe_rmsnorm_args* a) {
-    if (a->num_tokens < 0 || a->num_tokens > (1ll << 22)) return MOE_E_SHAPE;
+    if (a->num_tokens < 0 || a->num_tokens > (1ll << 20)) return MOE_E_SHAPE;
     if (a->hidden < 32 || a->hidden > 16384 || a->hidden % 32) return MOE_E_SHAPE;
     if (a->reserved || !(a->eps >= 0.0) || isinf(a->eps)) return MOE_E_OPTION;
     if (!is_float(a->x_dtype) || !is_float(a->weight_dtype)) return MOE_E_DTYPE;

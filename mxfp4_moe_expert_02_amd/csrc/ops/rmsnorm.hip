@@ -18,10 +18,36 @@
 namespace moe {
 namespace {
 
+// v's value of the lane that CTRL (a DPP control) names
+template <int CTRL>
+__device__ inline double dpp(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xf, 0xf, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ inline double lane_value(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// sum over the wave, the same in every lane (every lane takes part)
 __device__ inline double wave_sum(double v) {
-#pragma unroll
-    for (int m = 1; m < kWave; m <<= 1) v += __shfl_xor(v, m);
-    return v;
+    v += dpp<0xB1>(v);   // lanes 1, 0, 3, 2 of a quad
+    v += dpp<0x4E>(v);   // lanes 2, 3, 0, 1
+    v += dpp<0x141>(v);  // half a row mirrored: the other quad of 8
+    v += dpp<0x140>(v);  // a row mirrored: the other 8 of 16
+    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+
+// 1 / sqrt(m) for m >= 0: the hardware's estimate and two Newton steps (to
+// about 2^-52); 0 for infinity, as the quotient by sqrt(m) would give
+__device__ inline double rsqrt_full(double m) {
+    double r = __builtin_amdgcn_rsq(m);
+    r = r * fma(-0.5 * m * r, r, 1.5);
+    r = r * fma(-0.5 * m * r, r, 1.5);
+    return m == __builtin_inf() ? 0.0 : r;
 }
 
 // v with its low word folded into the last bit of the high one (set if any
@@ -43,7 +69,7 @@ constexpr int kNormPiece = 8;
 // (one row per workgroup); NP: pieces of 8 elements per thread.
 template <typename X, typename R, int WPR, int NP>
 __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR)
-rmsnorm_kernel(moe_rmsnorm_args a) {
+rmsnorm_kernel(moe_rmsnorm_args a, bool stream) {
     constexpr int kThreads = 64 * WPR;  // of a row
     __shared__ double part[WPR];
     const int tid = WPR == 1 ? threadIdx.x % 64 : threadIdx.x;
@@ -86,7 +112,7 @@ rmsnorm_kernel(moe_rmsnorm_args a) {
             float o[kNormPiece];
 #pragma unroll
             for (int e = 0; e < kNormPiece; e++) o[e] = sizeof(R) == 2 ? to_f32_odd(s[p][e]) : (float)s[p][e];
-            if (i < pieces) store_piece<kNormPiece>(ro + i * kNormPiece, o);
+            if (i < pieces) store_piece<kNormPiece>(ro + i * kNormPiece, o, stream);
         }
     }
     sum = wave_sum(sum);
@@ -97,7 +123,7 @@ rmsnorm_kernel(moe_rmsnorm_args a) {
 #pragma unroll
         for (int w = 0; w < WPR; w++) sum += part[w];
     }
-    const double rinv = 1.0 / sqrt(sum / H + a.eps);
+    const double rinv = rsqrt_full(sum / H + a.eps);
     uint16_t* y = a.y ? (uint16_t*)a.y + t * a.y_stride : nullptr;
 #pragma unroll
     for (int p = 0; p < NP; p++) {
@@ -110,7 +136,7 @@ rmsnorm_kernel(moe_rmsnorm_args a) {
             float o[kNormPiece];
 #pragma unroll
             for (int e = 0; e < kNormPiece; e++) o[e] = to_f32_odd(n[e]);
-            store_piece<kNormPiece>(y + i * kNormPiece, o);
+            store_piece<kNormPiece>(y + i * kNormPiece, o, stream);
         }
         if (!a.codes) continue;
         // a block of 32 lies in four neighbouring lanes, which agree on its
@@ -121,8 +147,8 @@ rmsnorm_kernel(moe_rmsnorm_args a) {
             const uint32_t hi = (uint32_t)(__builtin_bit_cast(uint64_t, n[e]) >> 32) & 0x7fffffffu;
             top = hi > top ? hi : top;
         }
-        top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+        top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xf, 0xf, true));
+        top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x4E, 0xf, 0xf, true));
         if (!live) continue;
         const bool bad = top >= 0x7ff00000u;  // a NaN or an infinity
         int se = (int)(top >> 20) - 1023 - 8;  // a zero or subnormal block: below -127
@@ -135,7 +161,7 @@ rmsnorm_kernel(moe_rmsnorm_args a) {
             for (int e = 0; e < 4; e++) q[e] = bad ? 0.f : (float)sticky(ldexp(n[4 * h + e], -se));
             code[h] = e4m3_pack4(q);
         }
-        *reinterpret_cast<uint2*>(a.codes + t * H + i * kNormPiece) = make_uint2(code[0], code[1]);
+        store8(a.codes + t * H + i * kNormPiece, make_uint2(code[0], code[1]), stream);
         if ((i & 3) == 0) a.scales[t * (H / 32) + i / 4] = bad ? 255 : (uint8_t)(se + 127);
     }
 }
@@ -144,11 +170,16 @@ template <typename X, typename R>
 hipError_t launch_typed(const moe_rmsnorm_args& a, hipStream_t stream) {
     const int pieces = (int)(a.hidden / kNormPiece);
     const unsigned T = (unsigned)a.num_tokens;
-    if (pieces <= 64) rmsnorm_kernel<X, R, 1, 1><<<(T + 3) / 4, 256, 0, stream>>>(a);
-    else if (pieces <= 256) rmsnorm_kernel<X, R, 4, 1><<<T, 256, 0, stream>>>(a);
-    else if (pieces <= 512) rmsnorm_kernel<X, R, 4, 2><<<T, 256, 0, stream>>>(a);
-    else if (pieces <= 1024) rmsnorm_kernel<X, R, 4, 4><<<T, 256, 0, stream>>>(a);
-    else rmsnorm_kernel<X, R, 4, 8><<<T, 256, 0, stream>>>(a);
+    const bool big = a.num_tokens * a.hidden * (a.y ? 4 : 2) > kStreamBytes;
+    // Waves per row: one piece per thread up to 4096 columns, two beyond (4096
+    // rows of 4096: 8 waves 28 us, 4 waves 30, 16 waves 37; of 7168: 8 x 2
+    // pieces 59, 16 x 1 61, 4 x 4 70; 2048 of 16384: 16 x 2 81, 8 x 4 91)
+    if (pieces <= 64) rmsnorm_kernel<X, R, 1, 1><<<(T + 3) / 4, 256, 0, stream>>>(a, big);
+    else if (pieces <= 128) rmsnorm_kernel<X, R, 2, 1><<<T, 128, 0, stream>>>(a, big);
+    else if (pieces <= 256) rmsnorm_kernel<X, R, 4, 1><<<T, 256, 0, stream>>>(a, big);
+    else if (pieces <= 512) rmsnorm_kernel<X, R, 8, 1><<<T, 512, 0, stream>>>(a, big);
+    else if (pieces <= 1024) rmsnorm_kernel<X, R, 8, 2><<<T, 512, 0, stream>>>(a, big);
+    else rmsnorm_kernel<X, R, 16, 2><<<T, 1024, 0, stream>>>(a, big);
     return hipGetLastError();
 }
 

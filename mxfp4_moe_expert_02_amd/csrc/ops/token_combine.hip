@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) token_combine_kernel(moe_combine_arg
 }
 
 template <typename R, typename O, int P>
-__global__ void __launch_bounds__(kThreads) token_combine_backward_kernel(moe_combine_args a) {
+__global__ void __launch_bounds__(kThreads) token_combine_backward_kernel(moe_combine_args a, bool stream) {
     const int64_t slot = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave;
     if (slot >= a.num_tokens * a.top_k) return;
     const int lane = threadIdx.x % kWave;
@@ -86,19 +86,32 @@ __global__ void __launch_bounds__(kThreads) token_combine_backward_kernel(moe_co
     R* d = a.drows ? (R*)a.drows + (int64_t)p * a.drows_stride : nullptr;
     const int pieces = (int)a.hidden / P;
     float dot = 0.f;
-    for (int i = lane; i < pieces; i += kWave) {
-        float gv[P], yv[P];
-        load_piece<P>(g + i * P, gv);
+    // two pieces of each row in flight (drows may be rows: every lane stores
+    // where it has loaded, and only after it)
+    for (int i = lane; i < pieces; i += 2 * kWave) {
+        const int i2 = i + kWave;
+        const bool two = i2 < pieces;
+        float gv[2][P], yv[2][P];
+        load_piece<P>(g + i * P, gv[0]);
+        if (two) load_piece<P>(g + i2 * P, gv[1]);
         if (a.dweights) {
-            load_piece<P>(y + i * P, yv);
+            load_piece<P>(y + i * P, yv[0]);
+            if (two) load_piece<P>(y + i2 * P, yv[1]);
 #pragma unroll
-            for (int e = 0; e < P; e++) dot = fmaf(gv[e], yv[e], dot);
+            for (int e = 0; e < P; e++) dot = fmaf(gv[0][e], yv[0][e], dot);
+            if (two)
+#pragma unroll
+                for (int e = 0; e < P; e++) dot = fmaf(gv[1][e], yv[1][e], dot);
         }
         if (d) {
-            float o[P];
 #pragma unroll
-            for (int e = 0; e < P; e++) o[e] = w * gv[e];
-            store_piece<P>(d + i * P, o);
+            for (int u = 0; u < 2; u++) {
+                if (u == 1 && !two) break;
+                float o[P];
+#pragma unroll
+                for (int e = 0; e < P; e++) o[e] = w * gv[u][e];
+                store_piece<P>(d + (u ? i2 : i) * P, o, stream);
+            }
         }
     }
     if (!a.dweights) return;
@@ -132,8 +145,9 @@ hipError_t backward_typed(const moe_combine_args& a, hipStream_t stream) {
                        whole_pieces(a.drows, a.drows_stride, sizeof(R), a.hidden, P);
     const int64_t slots = a.num_tokens * a.top_k;
     const unsigned grid = (unsigned)((slots + kThreads / kWave - 1) / (kThreads / kWave));
-    if (whole) token_combine_backward_kernel<R, O, P><<<grid, kThreads, 0, stream>>>(a);
-    else token_combine_backward_kernel<R, O, 1><<<grid, kThreads, 0, stream>>>(a);
+    const bool big = slots * a.hidden * (int64_t)sizeof(R) > kStreamBytes;
+    if (whole) token_combine_backward_kernel<R, O, P><<<grid, kThreads, 0, stream>>>(a, big);
+    else token_combine_backward_kernel<R, O, 1><<<grid, kThreads, 0, stream>>>(a, big);
     return hipGetLastError();
 }
 

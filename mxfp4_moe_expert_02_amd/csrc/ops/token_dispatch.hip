@@ -3,14 +3,15 @@
 //
 // The slots are cut into chunks of whole tokens (about kChunkSlots slots).
 //   1. one workgroup per chunk counts its slots per expert;
-//   2. one workgroup turns the counts into each chunk's first position per
-//      expert (and writes counts and offsets);
+//   2. with many chunks, one workgroup turns the counts into each chunk's
+//      first position per expert (and writes counts and offsets);
 //   3. workgroups of a few tokens each count the slots of their chunk that
 //      come before them, place their own, and copy their rows: a token's
 //      row is read once and written to its places.
-// Calls of one chunk or a few (up to kOneLaunchSlots slots) need no first
-// position from anywhere: every workgroup of step 3 counts all slots itself
-// and the call is one launch without workspace.
+// Up to kSumChunks chunks step 3 sums the chunks' counts itself (a launch of
+// one workgroup costs 12 us against 2 for the sums: 32768 slots, 128
+// experts), and up to kOneLaunchSlots slots it counts the slots themselves:
+// the call is then one launch without workspace.
 // Positions are integers counted in slot order: the result does not depend
 // on which workgroup runs when.
 #include "ops_internal.h"
@@ -22,13 +23,18 @@ constexpr int kThreads = 256;
 constexpr int kChunkSlots = 1024;
 constexpr int kMaxChunks = 2048;
 constexpr int kOneLaunchSlots = 4096;
+constexpr int kSumChunks = 64;
 constexpr int kMaxTokSlots = 64;  // slots of one gather workgroup, at least one token
 
 struct Plan {
     int chunk_tok, chunks;  // tokens per chunk, number of chunks
     int wg_tok, wgs;        // tokens per gather workgroup, workgroups per chunk
     bool one;               // one launch
+    bool sums;              // the last launch sums the chunks' counts
 };
+
+// where place_rows_kernel gets the positions before its own chunk from
+enum class First { kSlots, kCounts, kScanned };
 
 Plan make_plan(int64_t T, int k) {
     Plan p;
@@ -38,6 +44,7 @@ Plan make_plan(int64_t T, int k) {
     if (slots < kChunkSlots) slots = kChunkSlots;
     p.chunk_tok = p.one ? (int)T : (int)((slots + k - 1) / k);
     p.chunks = (int)((T + p.chunk_tok - 1) / p.chunk_tok);
+    p.sums = !p.one && p.chunks <= kSumChunks;
     p.wg_tok = kMaxTokSlots / k < 4 ? kMaxTokSlots / k : 4;
     // long chunks: a gather workgroup recounts its chunk, so it takes a fair share of it
     if (p.chunk_tok / 256 > p.wg_tok) p.wg_tok = p.chunk_tok / 256;
@@ -108,30 +115,45 @@ chunk_scan_kernel(int32_t* hist, int chunks, int E, int32_t* counts, int32_t* of
     }
 }
 
-// the bytes of one row copied to each of its places; V: bytes per thread and step
+// the bytes of one row copied to each of its places (4 loads of V in flight
+// per thread before the first store)
 template <typename V>
-__device__ inline void copy_row(const uint8_t* src, uint8_t* dst, int64_t row_bytes, const int* place, int k) {
-    for (int i = threadIdx.x; i < row_bytes / (int)sizeof(V); i += kThreads) {
-        const V v = reinterpret_cast<const V*>(src)[i];
-        for (int j = 0; j < k; j++)
-            if (place[j] >= 0) reinterpret_cast<V*>(dst + place[j] * row_bytes)[i] = v;
+__device__ inline void copy_row(const uint8_t* src, uint8_t* dst, int64_t row_bytes, const int* place, int k,
+                                bool stream) {
+    constexpr int kBatch = 4;
+    const int n = (int)(row_bytes / (int)sizeof(V));
+    for (int i0 = threadIdx.x; i0 < n; i0 += kBatch * kThreads) {
+        V v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) v[u] = reinterpret_cast<const V*>(src)[min(i0 + u * kThreads, n - 1)];
+        for (int j = 0; j < k; j++) {
+            if (place[j] < 0) continue;
+            V* d = reinterpret_cast<V*>(dst + place[j] * row_bytes);
+#pragma unroll
+            for (int u = 0; u < kBatch; u++) {
+                if (i0 + u * kThreads >= n) break;
+                if constexpr (sizeof(V) == 16) store16(d + i0 + u * kThreads, v[u], stream);
+                else d[i0 + u * kThreads] = v[u];
+            }
+        }
     }
 }
 
 __device__ inline void copy_rows(const uint8_t* src, uint8_t* dst, int64_t row_bytes, const int* place, int k,
-                                 int vec) {
-    if (vec == 16) copy_row<uint4>(src, dst, row_bytes, place, k);
-    else if (vec == 4) copy_row<uint32_t>(src, dst, row_bytes, place, k);
-    else if (vec == 2) copy_row<uint16_t>(src, dst, row_bytes, place, k);
-    else copy_row<uint8_t>(src, dst, row_bytes, place, k);
+                                 int vec, bool stream) {
+    if (vec == 16) copy_row<uint4>(src, dst, row_bytes, place, k, stream);
+    else if (vec == 4) copy_row<uint32_t>(src, dst, row_bytes, place, k, stream);
+    else if (vec == 2) copy_row<uint16_t>(src, dst, row_bytes, place, k, stream);
+    else copy_row<uint8_t>(src, dst, row_bytes, place, k, stream);
 }
 
-template <bool ONE>
+template <First FROM>
 __global__ void __launch_bounds__(kThreads)
 place_rows_kernel(moe_dispatch_args a, Plan p, const int32_t* first, int64_t row_bytes, int64_t x_row_bytes, int vec,
-                  int scale_bytes, int scale_vec) {
-    __shared__ int before[kMaxExperts];            // slots of the expert ahead of this workgroup's
-    __shared__ int all[ONE ? kMaxExperts : 1];
+                  int scale_bytes, int scale_vec, bool stream) {
+    constexpr bool kAll = FROM != First::kScanned;   // the offsets are formed here
+    __shared__ int before[kMaxExperts];              // slots of the expert ahead of this workgroup's
+    __shared__ int all[kAll ? kMaxExperts : 1];
     __shared__ int own[kMaxTokSlots], place[kMaxTokSlots];
     __shared__ int wave_sum[kThreads / kWave];
     const int E = (int)a.num_experts, k = a.top_k, tid = threadIdx.x;
@@ -143,21 +165,36 @@ place_rows_kernel(moe_dispatch_args a, Plan p, const int32_t* first, int64_t row
     if (t1 > a.num_tokens) t1 = a.num_tokens;
     if (t0 >= t1) return;
     for (int e = tid; e < E; e += kThreads) {
-        before[e] = ONE ? 0 : first[(int64_t)chunk * E + e];
-        if (ONE) all[e] = 0;
+        before[e] = kAll ? 0 : first[(int64_t)chunk * E + e];
+        if (kAll) all[e] = 0;
     }
     const int n = (int)(t1 - t0) * k;
     if (tid < n) own[tid] = a.ids[t0 * k + tid];
     __syncthreads();
-    const int64_t send = ONE ? a.num_tokens * k : t0 * k;
+    if (FROM == First::kCounts) {
+        const int cells = p.chunks * E;  // at most kSumChunks * kMaxExperts
+        for (int i0 = tid; i0 < cells; i0 += 8 * kThreads) {
+            int h[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) h[u] = i0 + u * kThreads < cells ? first[i0 + u * kThreads] : 0;
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                if (h[u] == 0) continue;
+                const int c = (i0 + u * kThreads) / E, e = i0 + u * kThreads - c * E;
+                atomicAdd(&all[e], h[u]);
+                if (c < chunk) atomicAdd(&before[e], h[u]);
+            }
+        }
+    }
+    const int64_t send = FROM == First::kSlots ? a.num_tokens * k : t0 * k;
     for (int64_t s = c0 * k + tid; s < send; s += kThreads) {
         const int e = a.ids[s];
         if (!held(e, E)) continue;
         if (s < t0 * k) atomicAdd(&before[e], 1);
-        if (ONE) atomicAdd(&all[e], 1);
+        if (FROM == First::kSlots) atomicAdd(&all[e], 1);
     }
     __syncthreads();
-    if (ONE) {  // four experts per thread: the offsets of all of them
+    if (kAll) {  // four experts per thread: the offsets of all of them
         int v[4], sum = 0, total;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -195,9 +232,9 @@ place_rows_kernel(moe_dispatch_args a, Plan p, const int32_t* first, int64_t row
     __syncthreads();
     for (int64_t t = t0; t < t1; t++) {
         const int* pl = place + (t - t0) * k;
-        copy_rows((const uint8_t*)a.x + t * x_row_bytes, (uint8_t*)a.rows, row_bytes, pl, k, vec);
+        copy_rows((const uint8_t*)a.x + t * x_row_bytes, (uint8_t*)a.rows, row_bytes, pl, k, vec, stream);
         if (a.row_scales)
-            copy_rows(a.x_scales + t * scale_bytes, a.row_scales, scale_bytes, pl, k, scale_vec);
+            copy_rows(a.x_scales + t * scale_bytes, a.row_scales, scale_bytes, pl, k, scale_vec, false);
     }
 }
 
@@ -236,17 +273,22 @@ hipError_t launch_dispatch(const moe_dispatch_args& a, hipStream_t stream) {
     const int srow = a.row_scales ? (int)(a.hidden / 32) : 0;
     const int svec = copy_bytes(a.x_scales, a.row_scales, srow, srow);
     const unsigned grid = (unsigned)(p.chunks * (int64_t)p.wgs);
+    const bool big = a.num_tokens * k * row > kStreamBytes;
     if (p.one) {
-        place_rows_kernel<true><<<grid, kThreads, 0, stream>>>(a, p, nullptr, row, xrow, vec, srow, svec);
+        place_rows_kernel<First::kSlots><<<grid, kThreads, 0, stream>>>(a, p, nullptr, row, xrow, vec, srow, svec, big);
         return hipGetLastError();
     }
     int32_t* hist = (int32_t*)a.workspace;
     chunk_count_kernel<<<p.chunks, kThreads, 0, stream>>>(a.ids, a.num_tokens * k, p.chunk_tok * k, E, hist);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
+    if (p.sums) {
+        place_rows_kernel<First::kCounts><<<grid, kThreads, 0, stream>>>(a, p, hist, row, xrow, vec, srow, svec, big);
+        return hipGetLastError();
+    }
     chunk_scan_kernel<<<1, 1024, 0, stream>>>(hist, p.chunks, E, a.counts, a.offsets);
     if ((err = hipGetLastError()) != hipSuccess) return err;
-    place_rows_kernel<false><<<grid, kThreads, 0, stream>>>(a, p, hist, row, xrow, vec, srow, svec);
+    place_rows_kernel<First::kScanned><<<grid, kThreads, 0, stream>>>(a, p, hist, row, xrow, vec, srow, svec, big);
     return hipGetLastError();
 }
 

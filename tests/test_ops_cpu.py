@@ -50,7 +50,7 @@ def test_rmsnorm_refusals(O):
                                          MOE_E_OPTION, MOE_E_SHAPE, MOE_OK)
     assert O.ops_lib().moe_rmsnorm(None, None) == MOE_E_NULL
     for kw in (dict(hidden=0), dict(hidden=31), dict(hidden=40), dict(hidden=16416), dict(num_tokens=-1),
-               dict(num_tokens=(1 << 22) + 1), dict(x_stride=255), dict(residual_stride=128), dict(y_stride=-256),
+               dict(num_tokens=(1 << 20) + 1), dict(x_stride=255), dict(residual_stride=128), dict(y_stride=-256),
                dict(residual_out=0x2000, residual_out_stride=512),
                dict(residual_dtype=MOE_DT_BF16, residual_out=0x1000, residual_out_stride=512)):
         assert _norm(O, **kw) == MOE_E_SHAPE, kw
