@@ -45,10 +45,10 @@ Plan make_plan(int64_t T, int k) {
     p.chunk_tok = p.one ? (int)T : (int)((slots + k - 1) / k);
     p.chunks = (int)((T + p.chunk_tok - 1) / p.chunk_tok);
     p.sums = !p.one && p.chunks <= kSumChunks;
-    p.wg_tok = kMaxTokSlots / k < 4 ? kMaxTokSlots / k : 4;
-    // long chunks: a gather workgroup recounts its chunk, so it takes a fair share of it
-    if (p.chunk_tok / 256 > p.wg_tok) p.wg_tok = p.chunk_tok / 256;
-    if (p.one && T < 1024) p.wg_tok = 1;
+    // one token a workgroup (4096 tokens to 8 places each: 115 us, 117 with
+    // four, 121 with eight); of long chunks, which every workgroup recounts, a
+    // fair share
+    p.wg_tok = p.chunk_tok / 256 > 1 ? p.chunk_tok / 256 : 1;
     if (p.wg_tok * k > kMaxTokSlots) p.wg_tok = kMaxTokSlots / k;
     p.wgs = (p.chunk_tok + p.wg_tok - 1) / p.wg_tok;
     return p;
