@@ -231,6 +231,21 @@ int moe_combine_backward(const moe_combine_args* args, void* stream);
  * (moe_combine with weights = NULL; `rows` is drows, `out` is dx). */
 int moe_dispatch_backward(const moe_combine_args* args, void* stream);
 
+/* ----------------------------------------- the expert layer on MXFP8 rows
+ * moe_mxfp4_forward_ex with activations that are in MXFP8 already (as
+ * moe_rmsnorm and moe_mxfp8_linear leave them): x_codes [num_tokens, hidden]
+ * and x_scales [num_tokens, hidden / 32], both 16-byte aligned, in place of
+ * x.  The same output bits as moe_mxfp4_forward_ex with MOE_ACT_MXFP8 on an
+ * x whose encoding they are, without the encoding pass.  opt == NULL: the
+ * plain call on weights in the tile layout; else opt->act_format must be
+ * MOE_ACT_MXFP8 and opt->router_weight NULL (MOE_E_OPTION: the router product
+ * reads bf16 rows).  Needs moe_mxfp4_init, and shares the layer's workspace
+ * and its rules.  Status codes as moe_mxfp4_forward_ex. */
+int moe_mxfp4_forward_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const float* router_logits,
+                          int64_t num_tokens, int32_t top_k, const uint8_t* W_gate_up,
+                          const uint8_t* W_down, const moe_mxfp4_scales* scales, void* out, void* stream,
+                          const moe_mxfp4_options* opt);
+
 #ifdef __cplusplus
 }
 #endif

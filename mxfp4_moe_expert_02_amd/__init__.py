@@ -22,6 +22,6 @@ from ._lib import (MOE_ACT_BF16, MOE_ACT_MXFP8, MOE_DT_BF16, MOE_DT_F32, MOE_DT_
                    tensor_desc)
 from ._ops import (MOE_EPI_GELU, MOE_EPI_NONE, MOE_EPI_SILU, MOE_EPI_SILU_MUL, moe_combine,
                    moe_combine_backward, moe_dispatch, moe_dispatch_backward, moe_dispatch_workspace,
-                   moe_mxfp8_linear, moe_mxfp8_linear_workspace, moe_rmsnorm)
+                   moe_mxfp4_forward_mx8, moe_mxfp8_linear, moe_mxfp8_linear_workspace, moe_rmsnorm)
 
 __all__ = [n for n in dir() if n.startswith(("moe_", "MOE_"))] + ["MoeError", "lib", "tensor_desc"]

@@ -24,7 +24,8 @@ MOE_EPI_GELU = 2
 MOE_EPI_SILU_MUL = 3
 
 OPS_EXPORTED = ("moe_rmsnorm", "moe_mxfp8_linear", "moe_mxfp8_linear_workspace", "moe_dispatch",
-                "moe_dispatch_workspace", "moe_dispatch_backward", "moe_combine", "moe_combine_backward")
+                "moe_dispatch_workspace", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+                "moe_mxfp4_forward_mx8")
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
@@ -88,7 +89,7 @@ def ops_lib() -> ctypes.CDLL:
     L = _lib.lib()
     if _ready is not L:
         for name in OPS_EXPORTED:
-            if name.endswith("_workspace"):
+            if name.endswith("_workspace") or name == "moe_mxfp4_forward_mx8":
                 continue
             getattr(L, name).restype, getattr(L, name).argtypes = ctypes.c_int, [_vp, _vp]
             _entry[name] = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, _vp)((name, L))
@@ -96,6 +97,9 @@ def ops_lib() -> ctypes.CDLL:
         L.moe_mxfp8_linear_workspace.argtypes = [_i64, _i64, _i64, _i32]
         L.moe_dispatch_workspace.restype = _i64
         L.moe_dispatch_workspace.argtypes = [_i64, _i64, _i32]
+        L.moe_mxfp4_forward_mx8.restype = ctypes.c_int
+        L.moe_mxfp4_forward_mx8.argtypes = [_vp, _vp, _vp, _i64, _i32, _vp, _vp, ctypes.POINTER(_lib.moe_mxfp4_scales),
+                                            _vp, _vp, ctypes.POINTER(_lib.moe_mxfp4_options)]
         _ready = L
     return L
 
@@ -301,3 +305,34 @@ def moe_combine_backward(dout, rows, weights, pos, drows=None, dweights=None, st
     return _call("moe_combine_backward",
                  _pack_combine(pr, _row(rows), pw, pp, 0, 0, pg, _row(dout), pd, ld_d, pdw, T, n, H, k,
                                _DT[rows.dtype], _DT[dout.dtype], 0), stream, check)
+
+
+def moe_mxfp4_forward_mx8(x_codes, x_scales, router_logits, top_k: int, W_gate_up, W_down, scales, out,
+                          shared=None, stream=None, check: bool = True) -> int:
+    """The expert layer on MXFP8 activations: moe_mxfp4_forward_ex with
+    MOE_ACT_MXFP8 on x_codes [T, H] and x_scales [T, H/32] uint8 in place of x.
+    router_logits [T, E] float32, out [T, H] bfloat16; W_gate_up, W_down and
+    scales in the tile layout (moe_mxfp4_prepack); shared as there."""
+    T, H = _matrix(x_codes, "x_codes", "[tokens, hidden]")
+    E, dev = _matrix(router_logits, "router_logits", "[tokens, experts]")[1], _dev(x_codes)
+    pc, ps = _want(x_codes, "x_codes", _U8, (T, H), dev), _want(x_scales, "x_scales", _U8, (T, H // 32), dev)
+    pl, po = _want(router_logits, "router_logits", _F32, (T, E), dev), _want(out, "out", _BF16, (T, H), dev)
+    inter2 = W_gate_up.numel() * 2 // (E * H)  # 2 I, from the byte count
+    weights = [(W_gate_up, E * inter2 * H // 2, "W_gate_up"), (W_down, E * H * inter2 // 4, "W_down"),
+               (scales[0], E * inter2 * H // 32, "scales[0]"), (scales[1], E * H * inter2 // 64, "scales[1]")]
+    if shared is not None:
+        weights += [(t, n, f"shared[{i}]") for i, (t, n) in enumerate(zip(
+            shared, (inter2 * H, inter2 * H // 32, H * inter2 // 2, H * inter2 // 64)))]
+    ptrs = []
+    for t, n, name in weights:
+        if t.numel() != n:
+            raise ValueError(f"{name}: expected {n} bytes, got {tuple(t.shape)}")
+        ptrs.append(_want(t, name, _U8, t.shape, dev))
+    opt = _lib.moe_mxfp4_options(act_format=_lib.MOE_ACT_MXFP8, weight_layout=_lib.MOE_LAYOUT_TILES)
+    if shared is not None:
+        opt.shared_gate_up, opt.shared_gate_up_scales, opt.shared_down, opt.shared_down_scales = ptrs[4:]
+    sc = _lib.moe_mxfp4_scales(ptrs[2], ptrs[3])
+    rc = ops_lib().moe_mxfp4_forward_mx8(pc, ps, pl, T, top_k, ptrs[0], ptrs[1], ctypes.byref(sc), po,
+                                         _current_stream(_device()) if stream is None else _lib._stream(stream),
+                                         ctypes.byref(opt))
+    return _check(rc, "moe_mxfp4_forward_mx8") if check else rc

@@ -20,7 +20,7 @@
 
 #include <mutex>
 
-#include "../../include/moe_mxfp4.h"
+#include "../../include/ops/moe_ops.h"
 #include "moe_internal.h"
 
 namespace {
@@ -280,10 +280,13 @@ int moe_mxfp4_forward_t(const moe_tensor* x, const moe_tensor* router_logits, in
                                 (const uint8_t*)W_down->data, &sc, out->data, stream, opt);
 }
 
-int moe_mxfp4_forward_ex(const void* x, const float* router_logits, int64_t num_tokens,
-                         int32_t top_k, const uint8_t* W_gate_up, const uint8_t* W_down,
-                         const moe_mxfp4_scales* scales, void* out, void* stream,
-                         const moe_mxfp4_options* opt) {
+namespace {
+
+// The layer on x, or (x null, MOE_ACT_MXFP8) on x already encoded: codes xq
+// and block scales xs.
+int forward(const void* x, const uint8_t* xq, const uint8_t* xs, const float* router_logits,
+            int64_t num_tokens, int32_t top_k, const uint8_t* W_gate_up, const uint8_t* W_down,
+            const moe_mxfp4_scales* scales, void* out, void* stream, const moe_mxfp4_options* opt) {
     moe_mxfp4_options o;
     memset(&o, 0, sizeof(o));
     if (opt) o = *opt;
@@ -309,7 +312,7 @@ int moe_mxfp4_forward_ex(const void* x, const float* router_logits, int64_t num_
         return MOE_E_OPTION;
     if (num_tokens == 0) return MOE_OK;
     if (o.router_weight) router_logits = nullptr;  // ignored: the layer computes the logits
-    if (!x || (!router_logits && !o.router_weight) || !W_gate_up || !W_down || !scales || !out)
+    if ((!x && !(xq && xs)) || (!router_logits && !o.router_weight) || !W_gate_up || !W_down || !scales || !out)
         return MOE_E_NULL;
     if (!scales->gate_up || !scales->down) return MOE_E_NULL;
     if (top_k < 1) return MOE_E_TOPK;
@@ -322,8 +325,8 @@ int moe_mxfp4_forward_ex(const void* x, const float* router_logits, int64_t num_
     if (!aligned16(o.shared_gate_up) || !aligned16(o.shared_gate_up_scales) ||
         !aligned16(o.shared_down) || !aligned16(o.shared_down_scales))
         return MOE_E_ALIGN;
-    if (!aligned16(x) || !aligned16(router_logits) || !aligned16(o.router_weight) ||
-        !aligned16(W_gate_up) ||
+    if (!aligned16(x) || !aligned16(xq) || !aligned16(xs) || !aligned16(router_logits) ||
+        !aligned16(o.router_weight) || !aligned16(W_gate_up) ||
         !aligned16(W_down) || !aligned16(scales->gate_up) || !aligned16(scales->down) ||
         !aligned16(out))
         return MOE_E_ALIGN;
@@ -383,9 +386,11 @@ int moe_mxfp4_forward_ex(const void* x, const float* router_logits, int64_t num_
     // the routing pass also runs for a self-routed layer when its results
     // are asked for (it writes the same ids and weights the layer uses)
     const bool want_route = o.ids || o.weights || o.counts || o.offsets || o.sorted;
-    if (mx8) {  // x is encoded in the routing stage (events [0]..[1])
+    if (mx8 && x) {  // x is encoded in the routing stage (events [0]..[1])
         err = moe::launch_quantize_x_mxfp8((const uint16_t*)x, T, H, ws->x_codes, ws->x_scales, st);
         if (err != hipSuccess) return hip_fail(err, "quantize x");
+        xq = ws->x_codes;
+        xs = ws->x_scales;
     }
     if (!self || want_route) {
         err = moe::launch_route(router_logits, T, E, k, *ws, 1 << 30, path, item_tok, st);
@@ -429,8 +434,8 @@ int moe_mxfp4_forward_ex(const void* x, const float* router_logits, int64_t num_
     a.pos = ws->pos;
     a.out = (uint16_t*)out;
     a.col_tiles = ws->col_tiles;
-    a.xq = ws->x_codes;
-    a.xs = ws->x_scales;
+    a.xq = xq;
+    a.xs = xs;
     a.hq = ws->h_codes;
     a.hs = ws->h_scales;
     a.queue = ws->queue;
@@ -532,8 +537,8 @@ int moe_mxfp4_forward_ex(const void* x, const float* router_logits, int64_t num_
         {o.ids, ws->ids, (size_t)S * 4},         {o.weights, ws->wts, (size_t)S * 4},
         {o.counts, ws->counts, (size_t)E * 4},   {o.offsets, ws->offsets, (size_t)(E + 1) * 4},
         {o.sorted, ws->sorted, (size_t)S * 4},
-        {mx8 ? o.x_codes : nullptr, ws->x_codes, (size_t)T * H},
-        {mx8 ? o.x_scales : nullptr, ws->x_scales, (size_t)T * (H / 32)},
+        {mx8 ? o.x_codes : nullptr, xq, (size_t)T * H},
+        {mx8 ? o.x_scales : nullptr, xs, (size_t)T * (H / 32)},
         {mx8 ? o.h_codes : nullptr, ws->h_codes, (size_t)S * I},
         {mx8 ? o.h_scales : nullptr, ws->h_scales, (size_t)S * (I / 32)},
         {o.wait_error, self_fused ? self_misc + moe::kSelfErrorOut : ws->queue + moe::kQueueError, 4},
@@ -545,6 +550,31 @@ int moe_mxfp4_forward_ex(const void* x, const float* router_logits, int64_t num_
         if (err != hipSuccess) return hip_fail(err, "hipMemcpyAsync(debug output)");
     }
     return MOE_OK;
+}
+
+}  // namespace
+
+int moe_mxfp4_forward_ex(const void* x, const float* router_logits, int64_t num_tokens,
+                         int32_t top_k, const uint8_t* W_gate_up, const uint8_t* W_down,
+                         const moe_mxfp4_scales* scales, void* out, void* stream,
+                         const moe_mxfp4_options* opt) {
+    return forward(x, nullptr, nullptr, router_logits, num_tokens, top_k, W_gate_up, W_down, scales, out,
+                   stream, opt);
+}
+
+int moe_mxfp4_forward_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const float* router_logits,
+                          int64_t num_tokens, int32_t top_k, const uint8_t* W_gate_up,
+                          const uint8_t* W_down, const moe_mxfp4_scales* scales, void* out, void* stream,
+                          const moe_mxfp4_options* opt) {
+    moe_mxfp4_options o;
+    memset(&o, 0, sizeof(o));
+    o.act_format = MOE_ACT_MXFP8;
+    o.weight_layout = MOE_LAYOUT_TILES;
+    if (opt) o = *opt;
+    // the router product reads bf16 rows, which this call does not have
+    if (o.act_format != MOE_ACT_MXFP8 || o.router_weight) return MOE_E_OPTION;
+    return forward(nullptr, x_codes, x_scales, router_logits, num_tokens, top_k, W_gate_up, W_down, scales,
+                   out, stream, &o);
 }
 
 int moe_mxfp4_forward(const void* x, const float* router_logits, int64_t num_tokens,

@@ -108,3 +108,66 @@ def order(ids, E):
         pos[s], srt[p] = p, s
         at[flat[s]] += 1
     return counts, offsets, srt, pos.reshape(ids.shape)
+
+
+STEP = 2.0 ** -23  # a float32 step, relative
+
+
+def linear(xc, xs, wc, ws, act="none", bias=None, res=None, tokens=None):
+    """act(x W^T + bias) + res of MXFP8 operands, before the output's rounding,
+    and how far a float32 evaluation of it may be off.
+
+    x and W are exact in MXFP8, and so is each product in float32 (two
+    four-bit significands).  The sum over K of them:
+      the bf16 matrix cores (up to 128 tokens) and the additions between
+      products: each partial sum is off by at most one float32 step of the
+      sum of magnitudes, (K + 1) * 2^-23 * (sum |x w| + |bias|) in all;
+      the FP8 matrix cores (more tokens): they add the 8 products of
+      consecutive k first, and drop what lies below 2^-13 of the largest one's
+      leading bit: each of the 8 is off by less than 2^-13 of the group's
+      largest magnitude, 8 * 2^-13 * (sum over groups of max |x w|) in all
+      (the typical error is far smaller: 1.4e-5 of the sum's rms).
+    The activation:
+      SiLU   moves by at most 1.1 dv, its own evaluation by (8 + |v|) * 2^-23 of
+             it (an exponential of an argument rounded at 2^-24 |v|, a
+             reciprocal, two products)
+      GELU   moves by at most 1.13 dv, its evaluation by (16 + 2 v^2) * 2^-23 of
+             it (erfc to a few steps, its argument rounded: relative
+             2 a^2 * 2^-23 for a = v / sqrt 2)"""
+    x, w = mx8_values(xc, xs), mx8_values(wc, ws)
+    T, K = x.shape
+    with np.errstate(invalid="ignore"):
+        v, mag = x @ w.T, np.abs(x) @ np.abs(w).T
+        if bias is not None:
+            v, mag = v + bias, mag + np.abs(bias)
+        dv = (K + 1) * STEP * mag
+        if (tokens or T) > 128:  # tokens: of the call, where x holds some of them
+            top = np.zeros_like(v)
+            for k in range(0, K, 8):
+                top += np.abs(x[:, None, k:k + 8] * w[None, :, k:k + 8]).max(-1)
+            dv = dv + 8 * 2.0 ** -13 * top
+        if act == "silu":
+            a = silu(v)
+            v, dv = a, 1.1 * dv + (8 + np.abs(v)) * STEP * np.abs(a)
+        elif act == "gelu":
+            a = gelu(v)
+            v, dv = a, 1.13 * dv + (16 + 2 * v * v) * STEP * np.abs(a)
+        elif act == "silu_mul":
+            h = v.shape[1] // 2
+            g, u, dg, du = v[:, :h], v[:, h:], dv[:, :h], dv[:, h:]
+            a = silu(g)
+            da = 1.1 * dg + (8 + np.abs(g)) * STEP * np.abs(a)
+            v, dv = a * u, np.abs(u) * da + np.abs(a) * du + da * du + STEP * np.abs(a * u)
+        if res is not None:
+            v = v + res
+            dv = dv + STEP * np.abs(v)
+    return v, dv + 2.0 ** -149
+
+
+def prepacked(M, codes: np.ndarray, scales: np.ndarray, pairs: bool):
+    """Row-major MXFP8 weights on the device in the tile layout."""
+    import torch
+    c, s = torch.from_numpy(np.ascontiguousarray(codes)).cuda(), torch.from_numpy(np.ascontiguousarray(scales)).cuda()
+    t, ts = torch.empty_like(c), torch.empty_like(s)
+    M.moe_mxfp8_prepack(c.view(1, *c.shape), s.view(1, *s.shape), t, ts, gate_up_pairs=pairs)
+    return t, ts

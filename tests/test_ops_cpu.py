@@ -197,6 +197,32 @@ def test_combine_refusals(O, fn):
             assert call(rows=0, dweights=0) == MOE_E_HIP
 
 
+@pytest.mark.skipif(gpu_available(), reason="no workspace exists only without a device")
+def test_forward_mx8_refusals(O):
+    import mxfp4_moe_expert_02_amd as M
+    from mxfp4_moe_expert_02_amd import _lib
+
+    def call(c=0x1000, s=0x2000, lg=0x3000, n=9, k=2, out=0x8000, opt=None):
+        sc = _lib.moe_mxfp4_scales(0x6000, 0x7000)
+        return O.ops_lib().moe_mxfp4_forward_mx8(c, s, lg, n, k, 0x4000, 0x5000, ctypes.byref(sc), out, None,
+                                                 None if opt is None else ctypes.byref(opt))
+
+    assert call() == M.MOE_E_NOT_INIT          # nothing to refuse but the missing workspace
+    assert call(n=0) == M.MOE_OK and call(n=-2) == M.MOE_E_SHAPE and call(k=0) == M.MOE_E_TOPK
+    for kw in (dict(c=0), dict(s=0), dict(lg=0), dict(out=0)):
+        assert call(**kw) == M.MOE_E_NULL, kw
+    for kw in (dict(c=0x1008), dict(s=0x2004), dict(out=0x8002)):
+        assert call(**kw) == M.MOE_E_ALIGN, kw
+    o = _lib.moe_mxfp4_options(M.MOE_ACT_MXFP8, 0)
+    assert call(opt=o) == M.MOE_E_OPTION       # row-major weights
+    o.weight_layout = M.MOE_LAYOUT_TILES
+    assert call(opt=o) == M.MOE_E_NOT_INIT
+    o.router_weight = 0x9000
+    assert call(opt=o) == M.MOE_E_OPTION       # the router product needs bf16 rows
+    o.router_weight, o.act_format = 0, M.MOE_ACT_BF16
+    assert call(opt=o) == M.MOE_E_OPTION
+
+
 def test_binding_refuses_other_memory(O):
     """Host tensors, wrong types, shapes and strides raise before any call."""
     import torch
