@@ -22,8 +22,6 @@
 namespace moe {
 namespace {
 
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
-
 __device__ inline i32x8_t operand(const uint4& lo, const uint4& hi) {
     return i32x8_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
@@ -335,10 +333,10 @@ __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear
 // 8 whole rows: with the rows' pieces spread over the lanes in operand order
 // instead (16 rows x 64 bytes per load) every quarter of a wave touches 16
 // cache lines, and the loads alone took 1.55 us a chunk against 0.6.
-// Products: v_mfma_scale_f32_32x32x64_f8f6f4, two per chunk (s = 0, 1).
-// Lane (r, h) = (l % 32, l / 32) of an operand holds the 16-byte pieces
-// 4s + h and 4s + h + 2 of row r's 128 bytes and the scale of block 2s + h;
-// of D rows 8j + 4h .. + 3 (j = 0 .. 3) of token r.
+// Products: v_mfma_scale_f32_16x16x128_f8f6f4, lane (r, g) of an operand
+// holding the 16-byte pieces g and g + 4 of row r's 128 bytes and the scale of
+// block g (from registers alone, on random data: 3.79 PFLOP/s; the 32x32x64
+// shape, whose clock falls further, 3.28).
 template <int RQ, int TT, int STAGES>
 struct TileSmem {
     alignas(16) uint8_t a[STAGES][RQ][8192];
@@ -361,21 +359,17 @@ __device__ inline void wait_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <int SA, int SB>
-__device__ inline f32x16_t mfma32(const i32x8_t& A, const i32x8_t& B, const f32x16_t& c, uint32_t sa, uint32_t sb) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 0, 0, SA, (int)sa, SB, (int)sb);
-}
-
 template <int ACT, bool MX, int RQ, int TT, int WR, int WT, int STAGES>
 __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_linear_args a, TileGrid p) {
     constexpr int kStages = STAGES, kWaves = WR * WT;
-    constexpr int Q = RQ / WR, NT = TT / WT;                   // a wave's quads and token tiles
+    constexpr int Q = RQ / WR, NT = TT * 2 / WT;               // a wave's quads and 16-token tiles
+    constexpr int NG = 4 * Q;                                  // and 16-row groups
     constexpr int kA = RQ * 8 / kWaves, kB = TT * 4 / kWaves;  // 1 KB loads per wave and chunk
     constexpr int kS = (RQ + TT / 2) / kWaves;                 // and 256-byte loads of block scales
     static_assert(RQ * 8 % kWaves == 0 && TT * 4 % kWaves == 0 && (RQ + TT / 2) % kWaves == 0, "loads per wave");
     extern __shared__ uint8_t smem_raw[];
     auto& sm = *reinterpret_cast<TileSmem<RQ, TT, kStages>*>(smem_raw);
-    const int w = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, c = lane % 32, h = lane / 32;
+    const int w = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
     // Workgroups go round the eight XCDs; each XCD takes a run of the tiles,
     // numbered down bands of kBand token blocks, so that what its L2 holds of
     // x and W serves several tiles (4096 x 7168 x 7168 from HBM: 206 us with
@@ -446,62 +440,53 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
         }
     };
     const int wr = w % WR, wt = w / WR;
-    f32x16_t acc[2 * Q][NT];
+    f32x4_t acc[NG][NT];
 #pragma unroll
-    for (int i = 0; i < 2 * Q; i++)
+    for (int i = 0; i < NG; i++)
 #pragma unroll
-        for (int t = 0; t < NT; t++) acc[i][t] = f32x16_t{};
-    // A: row r of 32 is row r % 16 of group r / 16; piece 4s + h (then + 2) is
-    // half h, lane r % 16 + 32 s (then + 16).  Its scale byte is that of the
-    // group: the odd group's is shifted down to the even one's place.
-    const int r = c % 16, a_at = c / 16 * 2048 + h * 1024 + r * 16, as_at = r + 16 * h, as_shift = c / 16 * 8;
-    const int b_at = c * 128 + (h ^ (c / 2 % 8)) * 16;
-    struct Operands {
-        i32x8_t A[2 * Q], B[NT];
-        uint32_t sa[Q], sb[NT];
-    } o0, o1;  // of the two products of a chunk
-    // one operand (B tiles first, then A tiles) of product s of the chunk in `buf`
-    constexpr int kUnits = NT + 2 * Q;
-    auto read = [&](Operands& o, int buf, auto s, auto n) {
-        constexpr int u = decltype(n)::value;
-        if constexpr (u < NT) {
-            const uint8_t* row = sm.b[buf][wt * NT + u];
-            o.B[u] = operand(*reinterpret_cast<const uint4*>(row + (b_at ^ (64 * s))),
-                             *reinterpret_cast<const uint4*>(row + (b_at ^ (64 * s + 32))));
-            o.sb[u] = sm.s[buf].b[(wt * NT + u) * 32 + c] >> (8 * h);
-        } else {
-            constexpr int q = (u - NT) / 2, i = (u - NT) % 2;
-            const uint8_t* qa = &sm.a[buf][wr * Q + q][a_at + 512 * s + i * 4096];
-            if (i == 0) o.sa[q] = sm.s[buf].a[wr * Q + q][as_at + 32 * s] >> as_shift;
-            o.A[u - NT] = operand(*reinterpret_cast<const uint4*>(qa), *reinterpret_cast<const uint4*>(qa + 256));
+        for (int t = 0; t < NT; t++) acc[i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const int a_at = (g & 1) * 1024 + (c + 16 * (g >> 1)) * 16;  // piece g; piece g + 4 is 512 bytes on
+    const int b_at = c * 128 + (g ^ (c / 2)) * 16;               // piece g; piece g + 4 is in slot ^ 4
+    i32x8_t A[NG], B[NT];
+    uint32_t sa[Q], sb[NT], sa_first = 0;  // sa_first: the next chunk's sa[0]
+    auto read_a = [&](int buf, auto i) {
+        const uint8_t* p = &sm.a[buf][wr * Q + i / 4][a_at + i % 4 * 2048];
+        A[i] = operand(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 512));
+        if constexpr (i % 4 == 0) {
+            const uint32_t v = sm.s[buf].a[wr * Q + i / 4][lane];
+            if constexpr (i == 0) sa_first = v;
+            else sa[i / 4] = v;
         }
     };
-    // the products of one operand set; after the n-th of them also(n) goes
-    // out, and the compiler keeps that order
-    constexpr int kMfma = 2 * Q * NT;
-    auto multiply = [&](const Operands& o, auto s, auto&& also) {
-        static_for<kMfma>([&](auto n) {
-            constexpr int i = decltype(n)::value / NT, t = decltype(n)::value % NT;
-            acc[i][t] = mfma32<2 * (i % 2), 2 * decltype(s)::value>(o.A[i], o.B[t], acc[i][t], o.sa[i / 2], o.sb[t]);
-            also(n);
-            __builtin_amdgcn_sched_barrier(0);
-        });
+    auto read_b = [&](int buf, auto t) {
+        const int row = (wt * NT + t) * 16;
+        const uint8_t* p = &sm.b[buf][0][row * 128];
+        B[t] = operand(*reinterpret_cast<const uint4*>(p + b_at), *reinterpret_cast<const uint4*>(p + (b_at ^ 64)));
+        sb[t] = reinterpret_cast<const uint8_t*>(&sm.s[buf].b[row + c])[g];
     };
-    // what goes out after product n of `count` steps spread over all of them
-    auto spread = [&](auto n, auto count, auto&& f) {
-        constexpr int lo = decltype(n)::value * decltype(count)::value / kMfma;
-        constexpr int hi = (decltype(n)::value + 1) * decltype(count)::value / kMfma;
+    // one product, after which also() goes out; the compiler keeps that order
+    auto product = [&](auto i, auto t, auto&& also) {
+        acc[i][t] = mfma_scaled<0, decltype(i)::value % 4, 0>(A[i], B[t], acc[i][t], sa[i / 4], sb[t]);
+        also();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // step n of `of` of something done in `count` parts
+    auto part = [&](auto n, auto of, auto count, auto&& f) {
+        constexpr int lo = decltype(n)::value * decltype(count)::value / decltype(of)::value;
+        constexpr int hi = (decltype(n)::value + 1) * decltype(count)::value / decltype(of)::value;
         static_for<hi - lo>([&](auto j) { f(std::integral_constant<int, lo + decltype(j)::value>{}); });
     };
-    const std::integral_constant<int, kUnits> units;
+    // A chunk in two phases.  First the groups up to kFirst, one after the
+    // other, while the rest of A is read kAheadA groups ahead; then this wave
+    // has read all of the chunk (lgkmcnt) and its loads of the next have
+    // landed (vmcnt), and past the barrier that holds for every wave.  Then
+    // the last groups, tile by tile: a tile of B done, its registers take the
+    // next chunk's, whose first groups of A are read and the loads of the
+    // chunk kStages on (over this one) go out meanwhile.
+    constexpr int kFirst = NG == 8 ? 5 : 2, kAheadA = NG == 8 ? 3 : 2, kLast = NG - kFirst;
+    const std::integral_constant<int, kLast * NT> in_second;
     const std::integral_constant<int, kLoads> loads;
-    // Operands are read half a chunk ahead: the first product's while the
-    // second of the chunk before runs.  In the middle of a chunk this wave
-    // has read all of it (lgkmcnt) and its loads of the next have landed
-    // (vmcnt); after the barrier that holds for every wave, so the next
-    // chunk can be read and the one kStages on loaded over this one.
-    const std::integral_constant<int, 0> s0;
-    const std::integral_constant<int, 1> s1;
+    const std::integral_constant<int, kAheadA> ahead;
     const int n_chunks = k1 - k0;
     static_for<kStages>([&](auto st) {
         if (st < n_chunks) static_for<kLoads>([&](auto n) { issue(n, st); });
@@ -509,32 +494,58 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
     // the first chunk's loads have landed (those of the others may be in flight)
     if (n_chunks >= kStages) wait_barrier<(kStages - 1) * kLoads>();
     else wait_barrier<0>();
-    static_for<kUnits>([&](auto n) { read(o0, 0, s0, n); });
+    static_for<NT>([&](auto t) { read_b(0, t); });
+    static_for<kAheadA>([&](auto i) { read_a(0, i); });
     int buf = 0;
     auto next = [&] { return buf + 1 == kStages ? 0 : buf + 1; };
-    auto first_half = [&] {
-        multiply(o0, s0, [&](auto n) { spread(n, units, [&](auto u) { read(o1, buf, s1, u); }); });
+    auto first_phase = [&] {
+        sa[0] = sa_first;
+        static_for<kFirst>([&](auto i) {
+            static_for<NT>([&](auto t) {
+                product(i, t, [&] {
+                    if constexpr (t == 0 && i + kAheadA < NG)
+                        read_a(buf, std::integral_constant<int, decltype(i)::value + kAheadA>{});
+                    if constexpr (t == NT / 2 && i == kFirst - 2)   // those beyond the last group's turn
+                        static_for<NG - kFirst - kAheadA + 1 < 0 ? 0 : NG - kFirst - kAheadA>([&](auto j) {
+                            read_a(buf, std::integral_constant<int, kFirst + kAheadA + decltype(j)::value>{});
+                        });
+                });
+            });
+        });
+    };
+    auto second_phase = [&](auto read_next, auto load_next) {
+        static_for<NT>([&](auto t) {
+            static_for<kLast>([&](auto j) {
+                constexpr int n = decltype(t)::value * kLast + decltype(j)::value;
+                product(std::integral_constant<int, kFirst + decltype(j)::value>{}, t, [&] {
+                    const std::integral_constant<int, n> at;
+                    if constexpr (decltype(load_next)::value)
+                        part(at, in_second, loads, [&](auto u) { issue(u, buf); });
+                    if constexpr (decltype(read_next)::value) {
+                        part(at, in_second, ahead, [&](auto u) { read_a(next(), u); });
+                        if constexpr (j == kLast - 1) read_b(next(), t);
+                    }
+                });
+            });
+        });
     };
     int k = 0;
     for (; k + kStages < n_chunks; k++) {
-        first_half();
+        first_phase();
         wait_barrier<(kStages - 2) * kLoads>();
-        multiply(o1, s1, [&](auto n) {
-            spread(n, units, [&](auto u) { read(o0, next(), s0, u); });
-            spread(n, loads, [&](auto u) { issue(u, buf); });
-        });
+        second_phase(std::true_type{}, std::true_type{});
         buf = next();
     }
     for (; k + 1 < n_chunks; k++) {  // nothing more to load
-        first_half();
+        first_phase();
         wait_barrier<0>();
-        multiply(o1, s1, [&](auto n) { spread(n, units, [&](auto u) { read(o0, next(), s0, u); }); });
+        second_phase(std::true_type{}, std::false_type{});
         buf = next();
     }
-    first_half();
-    multiply(o1, s1, [](auto) {});
+    first_phase();
+    second_phase(std::false_type{}, std::false_type{});
 
-    // The sums go through this wave's own part of the LDS, one token tile at
+    // The sums go through this wave's own part of the LDS, two token tiles at
     // a time, to lanes that hold 8 consecutive columns of a token: rows of 16
     // lanes then read the residual and write the output in 256-byte runs.
     constexpr bool kGated = ACT == MOE_EPI_SILU_MUL;
@@ -546,16 +557,18 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
     float(*mine)[kRow] = reinterpret_cast<float(*)[kRow]>(smem_raw + w * (32 * kRow * 4));
     const int64_t cols = kGated ? a.rows / 2 : a.rows;
     const int wq = q0 + wr * Q;                      // this wave's first quad
-    const int64_t tw = t0 + wt * NT * 32;            // and first token
+    const int64_t tw = t0 + wt * NT * 16;            // and first token
+    auto stage = [&](auto t) {  // token tiles 2t, 2t + 1
+#pragma unroll
+        for (int half = 0; half < 2; half++)
+#pragma unroll
+            for (int i = 0; i < NG; i++)
+                *reinterpret_cast<f32x4_t*>(&mine[16 * half + c][16 * i + 4 * g]) = acc[i][2 * t + half];
+        __builtin_amdgcn_wave_barrier();
+    };
     if (p.splits > 1) {
-        static_for<NT>([&](auto t) {
-#pragma unroll
-            for (int i = 0; i < 2 * Q; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    *reinterpret_cast<float4*>(&mine[c][32 * i + 8 * j + 4 * h]) =
-                        make_float4(acc[i][t][4 * j], acc[i][t][4 * j + 1], acc[i][t][4 * j + 2], acc[i][t][4 * j + 3]);
-            __builtin_amdgcn_wave_barrier();
+        static_for<NT / 2>([&](auto t) {
+            stage(t);
 #pragma unroll 2
             for (int n = 0; n < 32 * 8 * Q / kWave; n++) {
                 const int idx = n * kWave + lane, tok = idx / (8 * Q), o = idx % (8 * Q);
@@ -576,7 +589,7 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
         add8(bias, a.bias + c0);
         if (kGated) add8(bias_u, a.bias + cols + c0);
     }
-    static_for<NT>([&](auto t) {
+    static_for<NT / 2>([&](auto t) {
         uint4 res[kItems];
 #pragma unroll
         for (int n = 0; n < kItems; n++) {
@@ -584,13 +597,7 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
             res[n] = make_uint4(0, 0, 0, 0);
             if (a.residual && in && tok < a.num_tokens) res[n] = residual8(a, tok, c0);
         }
-#pragma unroll
-        for (int i = 0; i < 2 * Q; i++)
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                *reinterpret_cast<float4*>(&mine[c][32 * i + 8 * j + 4 * h]) =
-                    make_float4(acc[i][t][4 * j], acc[i][t][4 * j + 1], acc[i][t][4 * j + 2], acc[i][t][4 * j + 3]);
-        __builtin_amdgcn_wave_barrier();
+        stage(t);
 #pragma unroll
         for (int n = 0; n < kItems; n++) {
             const int row = n * (kWave / kOcts) + lane / kOcts;
