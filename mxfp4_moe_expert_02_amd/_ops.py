@@ -104,16 +104,18 @@ def ops_lib() -> ctypes.CDLL:
     return L
 
 
-# the current stream's handle without the Stream object around it (torch's own
-# generated code asks for it this way; 0.1 us against 3 us)
+# the current stream's handle without the Stream object around it, and the
+# current device without a check of the initialisation that a device tensor
+# has made (torch's own generated code asks this way; 0.1 us against 3 us and
+# 0.3)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: _lib._stream(None))
-_device = torch.cuda.current_device
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _call(name, packed, stream, check):
+def _call(name, packed, dev, stream, check):
     if _ready is None:
         ops_lib()
-    rc = _entry[name](packed, _current_stream(_device()) if stream is None else _lib._stream(stream))
+    rc = _entry[name](packed, _current_stream(dev) if stream is None else _lib._stream(stream))
     return _check(rc, name) if check and rc else rc
 
 
@@ -179,7 +181,7 @@ def moe_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None,
     pc = 0 if codes is None else _want(codes, "codes", _U8, shape, dev)
     ps = 0 if scales is None else _want(scales, "scales", _U8, (T, H // 32), dev)
     return _call("moe_rmsnorm", _pack_rmsnorm(px, _row(x), _DT[x.dtype], dt_r, pr, ld_r, po, ld_o, pw,
-                                              _DT[weight.dtype], 0, eps, py, ld_y, pc, ps, T, H), stream, check)
+                                              _DT[weight.dtype], 0, eps, py, ld_y, pc, ps, T, H), dev, stream, check)
 
 
 def moe_mxfp8_linear_workspace(num_tokens: int, rows: int, inner: int, activation: int = MOE_EPI_NONE) -> int:
@@ -218,7 +220,7 @@ def moe_mxfp8_linear(x_codes, x_scales, w_tiles, w_scales, out=None, out_codes=N
     if workspace is not None:
         pk, nw = _want(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel()
     return _call("moe_mxfp8_linear", _pack_linear(px, pxs, pw, pws, pb, pr, ld_r, po, ld_o, pc, ps, pk, nw, T, rows,
-                                                  K, activation, 0), stream, check)
+                                                  K, activation, 0), dev, stream, check)
 
 
 def moe_dispatch_workspace(num_tokens: int, num_experts: int, top_k: int) -> int:
@@ -261,7 +263,7 @@ def moe_dispatch(x, ids, num_experts: int, offsets, sorted, pos, rows, workspace
     if workspace is not None:
         pk, nw = _want(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel()
     return _call("moe_dispatch", _pack_dispatch(pi, px, ld_x, pxs, pn, pf, pt, pp, pr, prs, pk, nw, T, num_experts, H,
-                                                k, dt), stream, check)
+                                                k, dt), dev, stream, check)
 
 
 def _combine(name, rows, weights, pos, out, stream, check):
@@ -272,7 +274,7 @@ def _combine(name, rows, weights, pos, out, stream, check):
     pw = 0 if weights is None else _want(weights, "weights", _F32, slots, dev)
     pr, po = _want(rows, "rows", _FLOATS, (n, H), dev, True), _want(out, "out", _FLOATS, (T, H), dev, True)
     return _call(name, _pack_combine(pr, _row(rows), pw, pp, po, _row(out), 0, 0, 0, 0, 0, T, n, H, k,
-                                     _DT[rows.dtype], _DT[out.dtype], 0), stream, check)
+                                     _DT[rows.dtype], _DT[out.dtype], 0), dev, stream, check)
 
 
 def moe_combine(rows, weights, pos, out, stream=None, check: bool = True) -> int:
@@ -304,7 +306,7 @@ def moe_combine_backward(dout, rows, weights, pos, drows=None, dweights=None, st
     pdw = 0 if dweights is None else _want(dweights, "dweights", _F32, slots, dev)
     return _call("moe_combine_backward",
                  _pack_combine(pr, _row(rows), pw, pp, 0, 0, pg, _row(dout), pd, ld_d, pdw, T, n, H, k,
-                               _DT[rows.dtype], _DT[dout.dtype], 0), stream, check)
+                               _DT[rows.dtype], _DT[dout.dtype], 0), dev, stream, check)
 
 
 def moe_mxfp4_forward_mx8(x_codes, x_scales, router_logits, top_k: int, W_gate_up, W_down, scales, out,
@@ -333,6 +335,6 @@ def moe_mxfp4_forward_mx8(x_codes, x_scales, router_logits, top_k: int, W_gate_u
         opt.shared_gate_up, opt.shared_gate_up_scales, opt.shared_down, opt.shared_down_scales = ptrs[4:]
     sc = _lib.moe_mxfp4_scales(ptrs[2], ptrs[3])
     rc = ops_lib().moe_mxfp4_forward_mx8(pc, ps, pl, T, top_k, ptrs[0], ptrs[1], ctypes.byref(sc), po,
-                                         _current_stream(_device()) if stream is None else _lib._stream(stream),
+                                         _current_stream(dev) if stream is None else _lib._stream(stream),
                                          ctypes.byref(opt))
     return _check(rc, "moe_mxfp4_forward_mx8") if check else rc

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear
             multiply(wb[d % D], i + d, d % D);
             if (i + D + d < n) load(wb[d % D], seg + i + D + d, d % D);
         });
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // the next segment's scales go over these
     }
     __syncthreads();
 #pragma unroll

@@ -41,6 +41,11 @@ int check_norm(moe_rmsnorm_args* a) {
         if (a->residual_dtype != a->x_dtype) return MOE_E_DTYPE;
         if (a->residual_out_stride != a->x_stride) return MOE_E_SHAPE;
     }
+    if (a->y && a->y == a->residual_out) return MOE_E_OPTION;
+    if (a->y && a->y == a->x) {
+        if (a->x_dtype != MOE_DT_BF16) return MOE_E_DTYPE;
+        if (a->y_stride != a->x_stride) return MOE_E_SHAPE;
+    }
     if (misaligned(a->x, 16) || misaligned(a->residual, 16) || misaligned(a->residual_out, 16) ||
         misaligned(a->weight, 16) || misaligned(a->y, 16) || misaligned(a->codes, 16) || misaligned(a->scales, 4))
         return MOE_E_ALIGN;

@@ -54,9 +54,11 @@ def test_rmsnorm_refusals(O):
                dict(residual_out=0x2000, residual_out_stride=512),
                dict(residual_dtype=MOE_DT_BF16, residual_out=0x1000, residual_out_stride=512)):
         assert _norm(O, **kw) == MOE_E_SHAPE, kw
-    for kw in (dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(reserved=1)):
+    assert _norm(O, y=0x1000, y_stride=512) == MOE_E_SHAPE      # over x, but not row for row
+    for kw in (dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(reserved=1), dict(y=0x3000)):
         assert _norm(O, **kw) == MOE_E_OPTION, kw
-    for kw in (dict(x_dtype=MOE_DT_U8), dict(residual_dtype=0), dict(weight_dtype=9), dict(residual_out=0x1000)):
+    for kw in (dict(x_dtype=MOE_DT_U8), dict(residual_dtype=0), dict(weight_dtype=9), dict(residual_out=0x1000),
+               dict(y=0x1000, x_dtype=2)):
         assert _norm(O, **kw) == MOE_E_DTYPE, kw
     for kw in (dict(x=0), dict(weight=0), dict(y=0, codes=0, scales=0), dict(codes=0), dict(scales=0),
                dict(residual=0)):
