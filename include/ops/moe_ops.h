@@ -101,9 +101,9 @@ int moe_rmsnorm(const moe_rmsnorm_args* args, void* stream);
  *   out = act(v) + residual
  *
  * Up to 128 tokens the products and sums are float32's (about 1e-7 of the
- * sum's rms).  With more tokens the FP8 matrix cores add the products of 8
- * consecutive k to 13 bits below the largest of them before the float32
- * sum: an error of about 1.5e-5 of the sum's rms, at most 2^-10 of the
+ * sum's rms).  With more tokens the FP8 matrix cores may be used, which add
+ * the products of 8 consecutive k to 13 bits below the largest of them before
+ * the float32 sum: an error of about 1.5e-5 of the sum's rms, at most 2^-10 of the
  * largest product of each 8.  Values of x and W outside float32's normal
  * range may count as zero or infinity.
  *

@@ -359,8 +359,11 @@ __device__ inline void wait_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// Two waves per SIMD: with registers for one only the compiler keeps the sums
+// of 256 threads in accumulation registers and copies them around the second
+// phase (288 x 7168 x 7168: 39.2 us, 35.4 without).
 template <int ACT, bool MX, int RQ, int TT, int WR, int WT, int STAGES>
-__global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_linear_args a, TileGrid p) {
+__global__ void __launch_bounds__(WR * WT * kWave, 2) linear_tile_kernel(moe_mxfp8_linear_args a, TileGrid p) {
     constexpr int kStages = STAGES, kWaves = WR * WT;
     constexpr int Q = RQ / WR, NT = TT * 2 / WT;               // a wave's quads and 16-token tiles
     constexpr int NG = 4 * Q;                                  // and 16-row groups
@@ -477,13 +480,16 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
         static_for<hi - lo>([&](auto j) { f(std::integral_constant<int, lo + decltype(j)::value>{}); });
     };
     // A chunk in two phases.  First the groups up to kFirst, one after the
-    // other, while the rest of A is read kAheadA groups ahead; then this wave
+    // other, while the rest of A is read, a group a product; then this wave
     // has read all of the chunk (lgkmcnt) and its loads of the next have
     // landed (vmcnt), and past the barrier that holds for every wave.  Then
     // the last groups, tile by tile: a tile of B done, its registers take the
-    // next chunk's, whose first groups of A are read and the loads of the
-    // chunk kStages on (over this one) go out meanwhile.
-    constexpr int kFirst = NG == 8 ? 5 : 2, kAheadA = NG == 8 ? 3 : 2, kLast = NG - kFirst;
+    // next chunk's, whose first kAheadA groups of A are read and the loads of the
+    // chunk kStages on (over this one) go out meanwhile.  A short first phase
+    // leaves B's reads more time (4 groups: 34.3 us with 1, 35.8 with 2, 37.0
+    // with 3, 288 x 7168 x 7168), a long one A's (8 groups: 200 us with 5, 201
+    // with 4, 208 with 3, 4096 x 7168 x 7168).
+    constexpr int kFirst = NG == 8 ? 5 : 1, kAheadA = NG == 8 ? 3 : 2, kLast = NG - kFirst;
     const std::integral_constant<int, kLast * NT> in_second;
     const std::integral_constant<int, kLoads> loads;
     const std::integral_constant<int, kAheadA> ahead;
@@ -503,12 +509,8 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
         static_for<kFirst>([&](auto i) {
             static_for<NT>([&](auto t) {
                 product(i, t, [&] {
-                    if constexpr (t == 0 && i + kAheadA < NG)
-                        read_a(buf, std::integral_constant<int, decltype(i)::value + kAheadA>{});
-                    if constexpr (t == NT / 2 && i == kFirst - 2)   // those beyond the last group's turn
-                        static_for<NG - kFirst - kAheadA + 1 < 0 ? 0 : NG - kFirst - kAheadA>([&](auto j) {
-                            read_a(buf, std::integral_constant<int, kFirst + kAheadA + decltype(j)::value>{});
-                        });
+                    constexpr int next_a = decltype(i)::value * NT + decltype(t)::value + kAheadA;
+                    if constexpr (next_a < NG) read_a(buf, std::integral_constant<int, next_a>{});
                 });
             });
         });
@@ -613,9 +615,13 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
 }
 
 // ------------------------------------------------------------ the choice
-constexpr int kRowsMaxTok = 128;   // tokens of linear_rows_kernel
-constexpr int kSplitMaxTok = 1024;  // most tokens whose inner axis is split
+// Tokens of linear_rows_kernel: at 128 it is exact at about the tiles' speed
+// (128 x 4096 x 7168: 17.9 us, tiles 19.2; 128 x 7168 x 7168: 24.7 and 22.1).
+constexpr int kRowsMaxTok = 128, kRowsMostTok = 1024;
+constexpr int64_t kRowsMostWork = (int64_t)256 * 6144;  // workgroups times inner axis
+constexpr int kWideTiles = 160;    // from as many on 256 x 256 tiles
 constexpr int kMaxSplits = 8;
+constexpr int kSplitTok = 8192;    // most tokens times splits (the workspace's bound)
 constexpr int kCus = 256;
 
 struct LinearPlan {
@@ -632,15 +638,34 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
     LinearPlan p{};
     const int tiles = (int)((T + 15) / 16), chunks = (int)(inner / 128);
     const bool gated = activation == MOE_EPI_SILU_MUL;
-    p.rows = T <= kRowsMaxTok;
+    // linear_rows_kernel: few tokens, and more where its largest workgroups (64 rows x 64 tokens)
+    // all run at once and the work is small, so that the tiles' launches of few
+    // workgroups would mostly wait (320 x 2048 x 2048: 8.2 us, tiles 13.6; 1024
+    // x 1024 x 1024: 8.0 and 10.6; 192 x 4096 x 7168: 19.4 and 20.0; past the
+    // bound 1024 x 1024 x 8192: 26.9 and 23.4)
+    const int64_t most = rows / 64 * ((T + 63) / 64);
+    p.rows = T <= kRowsMaxTok || (T <= kRowsMostTok && most <= kCus && most * inner <= kRowsMostWork);
     int64_t splits = 1;
     if (!p.rows) {
+        // 256 x 256 tiles move half the bytes per product, 128 x 128 leave fewer
+        // CUs idle (1536 x 7168 x 7168: 168 wide tiles 86 us, narrow ones 106;
+        // 1024 x 7168 x 7168: 112 wide tiles 82 us, narrow ones 66)
         const int64_t wide_blocks = (rows + 255) / 256 * ((T + 255) / 256);
-        p.wide = wide_blocks >= 192;
+        p.wide = wide_blocks >= kWideTiles;
         const int n = p.wide ? 256 : 128;
         p.tile.row_blocks = (int)((rows + n - 1) / n);
         p.tile.tok_blocks = (int)((T + n - 1) / n);
-        if (!p.wide && T <= kSplitMaxTok) splits = kCus / ((int64_t)p.tile.row_blocks * p.tile.tok_blocks);
+        // A 128-k chunk of a workgroup takes about 0.5 us, the pass over the
+        // split sums 2 us and 0.5 us per MB of them; the number of splits that
+        // leaves the least, of those that fit on the CUs (1024 x 2048 x 6144:
+        // 28.6 us in 2, 30.8 in 1; x 2048: 23.2 and 14.6).
+        const int64_t blocks = (int64_t)p.tile.row_blocks * p.tile.tok_blocks;
+        const int64_t sums = T * rows * 4 / 1000000;  // MB
+        int64_t best = chunks;                        // in units of 0.5 us
+        for (int64_t n = 2; !p.wide && n <= kMaxSplits && n * blocks <= kCus && n * T <= kSplitTok; n++) {
+            const int64_t t = (chunks + n - 1) / n + 4 + n * sums;
+            if (t < best) best = t, splits = n;
+        }
     } else {
         // Of the tile shapes, the one whose workgroups come closest to one
         // per CU from below: fewer leave CUs idle, more take a second round

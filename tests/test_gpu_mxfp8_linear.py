@@ -70,7 +70,7 @@ class Case:
 
 
 @pytest.mark.parametrize("T", [1, 2, 9, 15, 16, 17, 31, 32, 33, 48, 63, 64, 65, 96, 127, 128, 129, 200, 255, 257, 300,
-                               513, 1025])
+                               513, 1025, 1040, 1055, 1057, 1151, 1279, 1281])
 @pytest.mark.parametrize("rows,K", [(64, 128), (192, 384), (512, 1152)])
 def test_every_token_count(M, T, rows, K):
     say(f"linear T={T} rows={rows} K={K}")
@@ -81,7 +81,7 @@ def test_every_token_count(M, T, rows, K):
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "silu_mul"])
 @pytest.mark.parametrize("out", ["bf16", "mxfp8"])
 @pytest.mark.parametrize("bias,residual", [(False, False), (True, False), (False, True), (True, True)])
-@pytest.mark.parametrize("T", [3, 40, 150, 400])
+@pytest.mark.parametrize("T", [3, 40, 150, 1060])
 def test_every_epilogue(M, act, out, bias, residual, T):
     say(f"linear act={act} out={out} bias={bias} residual={residual} T={T}")
     c = Case(M, T, 320, 640, act, bias, residual, out, seed=1)
@@ -89,7 +89,7 @@ def test_every_epilogue(M, act, out, bias, residual, T):
 
 
 @pytest.mark.parametrize("T,rows,K", [(1, 64, 7168), (16, 64, 65536), (9, 6144, 2048), (72, 4096, 7168), (72, 64, 7168),
-                                      (288, 512, 6144), (1001, 1024, 512), (2050, 512, 256), (5, 16384, 128),
+                                      (288, 512, 6144), (400, 6144, 1024), (1001, 2048, 512), (2050, 512, 256), (5, 16384, 128),
                                       (130, 8192, 256)])
 def test_real_shapes(M, T, rows, K):
     say(f"linear T={T} rows={rows} K={K}")
@@ -100,7 +100,7 @@ def test_real_shapes(M, T, rows, K):
 
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "silu_mul"])
 @pytest.mark.parametrize("out", ["bf16", "mxfp8"])
-@pytest.mark.parametrize("T", [9, 100, 150, 300])
+@pytest.mark.parametrize("T", [9, 100, 150, 1100])
 def test_epilogues_of_a_split_sum(M, act, out, T):
     """An inner axis long enough to be split over workgroups."""
     say(f"linear split act={act} out={out} T={T}")
@@ -125,7 +125,7 @@ def test_large_grids(M, T, rows, K, act, out):
     c.check(o, sorted(e for e in edges if e < T))
 
 
-@pytest.mark.parametrize("T", [9, 50, 300])
+@pytest.mark.parametrize("T", [9, 50, 1100])
 def test_strided_rows_and_in_place(M, T):
     import torch
     say(f"linear strided T={T}")
@@ -138,7 +138,7 @@ def test_strided_rows_and_in_place(M, T):
     assert (wide[:, :200] == 3).all() and (wide[:, 392:] == 3).all() and (wide[T] == 3).all()
 
 
-@pytest.mark.parametrize("T", [4, 70, 300])
+@pytest.mark.parametrize("T", [4, 70, 300, 1100])
 @pytest.mark.parametrize("out", ["bf16", "mxfp8"])
 def test_nan_blocks_stay_where_they_are(M, T, out):
     """A NaN block of one weight row reaches its column alone, one of a token
@@ -155,7 +155,7 @@ def test_nan_blocks_stay_where_they_are(M, T, out):
     c.check(c.run(M))
 
 
-@pytest.mark.parametrize("T", [4, 70, 300])
+@pytest.mark.parametrize("T", [4, 70, 300, 1100])
 def test_wide_range_of_scales(M, T):
     """Blocks of very different scales in one row, far from 1 (products down
     to 2^-80 and up to 2^80)."""
@@ -170,7 +170,7 @@ def test_wide_range_of_scales(M, T):
     c.check(c.run(M))
 
 
-@pytest.mark.parametrize("T", [64, 200])
+@pytest.mark.parametrize("T", [64, 200, 1100])
 def test_small_products_beside_large_ones(M, T):
     """One large product in each group of 8 consecutive k and small ones at
     every distance below it: up to 128 tokens all of them count, beyond it
@@ -195,7 +195,7 @@ def test_exact_small_integers(M):
     whatever the order of the sum."""
     say("linear integers")
     rng = np.random.default_rng(7)
-    for T in (7, 90, 310):
+    for T in (7, 90, 310, 1050):
         c = Case(M, T, 256, 1024, seed=8)
         x, w = rng.integers(-3, 4, size=(T, 1024)), rng.integers(-3, 4, size=(256, 1024))
         c.xc, c.xs = encode(x)
@@ -213,19 +213,19 @@ def test_no_tokens_and_determinism(M):
     e = lambda n: torch.empty(0, n, dtype=torch.uint8, device="cuda")
     assert M.moe_mxfp8_linear(e(128), e(4), c.dev["w_tiles"], c.dev["w_scales"],
                               out=torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")) == M.MOE_OK
-    for T in (9, 72, 300, 600):
+    for T in (9, 72, 300, 600, 1100):
         c = Case(M, T, 1024, 2048, seed=9)
         a, b = c.run(M), c.run(M)
         assert torch.equal(a["out"], b["out"])
 
 
-@pytest.mark.parametrize("T", [9, 72, 600])
-def test_streams_and_graphs(M, T):
+@pytest.mark.parametrize("T,rows", [(9, 1024), (72, 1024), (600, 1024), (600, 4096), (1100, 256)])
+def test_streams_and_graphs(M, T, rows):
     """A call on a stream of its own; two captured calls with workspaces of
     their own replayed side by side on changed inputs give the eager bits."""
     import torch
-    say(f"linear graphs T={T}")
-    cs = [Case(M, T, 1024, 2048, "silu", True, True, seed=10 + i) for i in range(2)]
+    say(f"linear graphs T={T} rows={rows}")
+    cs = [Case(M, T, rows, 2048, "silu", True, True, seed=10 + i) for i in range(2)]
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
     cs[0].check(cs[0].run(M, stream=st))
@@ -238,7 +238,7 @@ def test_streams_and_graphs(M, T):
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     for rnd in range(3):
         for i, (c, o) in enumerate(zip(cs, outs)):
-            n = Case(M, T, 1024, 2048, "silu", True, True, seed=30 + 2 * rnd + i)
+            n = Case(M, T, rows, 2048, "silu", True, True, seed=30 + 2 * rnd + i)
             for name in ("x_codes", "x_scales"):
                 c.dev[name].copy_(n.dev[name])
             o["out"].zero_()
