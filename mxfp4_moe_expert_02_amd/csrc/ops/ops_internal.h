@@ -81,43 +81,6 @@ __device__ inline void store_piece(float* p, const float (&v)[N]) {
     }
 }
 
-// The same past the caches' own lines where `stream` says so: results far
-// larger than the L2s (32 MB together) push out what the kernel still reads
-// if they are kept.
-constexpr int64_t kStreamBytes = 32 << 20;
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-__device__ inline void store16(void* p, const uint4& v, bool stream) {
-    if (stream) __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4_t*>(p));
-    else *reinterpret_cast<uint4*>(p) = v;
-}
-__device__ inline void store8(void* p, const uint2& v, bool stream) {
-    if (stream) __builtin_nontemporal_store(u32x2_t{v.x, v.y}, reinterpret_cast<u32x2_t*>(p));
-    else *reinterpret_cast<uint2*>(p) = v;
-}
-template <int N>
-__device__ inline void store_piece(uint16_t* p, const float (&v)[N], bool stream) {
-    if constexpr (N == 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            w[i] = (uint32_t)f32_to_bf16_rne(v[2 * i]) | ((uint32_t)f32_to_bf16_rne(v[2 * i + 1]) << 16);
-        store16(p, make_uint4(w[0], w[1], w[2], w[3]), stream);
-    } else {
-        store_piece<N>(p, v);
-    }
-}
-template <int N>
-__device__ inline void store_piece(float* p, const float (&v)[N], bool stream) {
-    if constexpr (N == 1) {
-        *p = v[0];
-    } else {
-#pragma unroll
-        for (int i = 0; i < N / 4; i++)
-            store16(p + 4 * i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                          __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])), stream);
-    }
-}
-
 // A value's E4M3 codes come from v_cvt_scalef32_pk_fp8_f32 (two values,
 // nearest even, subnormals included, not saturating): |v| is clamped to 448
 // first, the format's largest value.

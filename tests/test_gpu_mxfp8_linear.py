@@ -89,7 +89,7 @@ def test_every_epilogue(M, act, out, bias, residual, T):
 
 
 @pytest.mark.parametrize("T,rows,K", [(1, 64, 7168), (16, 64, 65536), (9, 6144, 2048), (72, 4096, 7168), (72, 64, 7168),
-                                      (288, 512, 6144), (400, 6144, 1024), (1001, 2048, 512), (2050, 512, 256), (5, 16384, 128),
+                                      (288, 512, 6144), (400, 6144, 256), (1001, 2048, 512), (2050, 512, 256), (5, 16384, 128),
                                       (130, 8192, 256)])
 def test_real_shapes(M, T, rows, K):
     say(f"linear T={T} rows={rows} K={K}")
@@ -219,7 +219,7 @@ def test_no_tokens_and_determinism(M):
         assert torch.equal(a["out"], b["out"])
 
 
-@pytest.mark.parametrize("T,rows", [(9, 1024), (72, 1024), (600, 1024), (600, 4096), (1100, 256)])
+@pytest.mark.parametrize("T,rows", [(9, 1024), (72, 1024), (600, 1024), (1100, 256)])
 def test_streams_and_graphs(M, T, rows):
     """A call on a stream of its own; two captured calls with workspaces of
     their own replayed side by side on changed inputs give the eager bits."""
