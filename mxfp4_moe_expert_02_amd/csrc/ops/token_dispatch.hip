@@ -120,7 +120,8 @@ chunk_scan_kernel(int32_t* hist, int chunks, int E, int32_t* counts, int32_t* of
 }
 
 // the bytes of one row copied to each of its places (4 loads of V in flight
-// per thread before the first store)
+// per thread before the first store; V a vector type of the compiler's, whose
+// copies stay whole: with the uint4 structure 147 us for 4096 tokens, not 115)
 template <typename V>
 __device__ inline void copy_row(const uint8_t* src, uint8_t* dst, int64_t row_bytes, const int* place, int k) {
     constexpr int kBatch = 4;
@@ -143,7 +144,7 @@ __device__ inline void copy_row(const uint8_t* src, uint8_t* dst, int64_t row_by
 
 __device__ inline void copy_rows(const uint8_t* src, uint8_t* dst, int64_t row_bytes, const int* place, int k,
                                  int vec) {
-    if (vec == 16) copy_row<uint4>(src, dst, row_bytes, place, k);
+    if (vec == 16) copy_row<u32x4_t>(src, dst, row_bytes, place, k);
     else if (vec == 4) copy_row<uint32_t>(src, dst, row_bytes, place, k);
     else if (vec == 2) copy_row<uint16_t>(src, dst, row_bytes, place, k);
     else copy_row<uint8_t>(src, dst, row_bytes, place, k);
