@@ -5,19 +5,23 @@
 // 256 scale bytes [lane][group], lane (r, g) = (l % 16, l / 16) holding block
 // g (k = 32g .. 32g+31) of row r.
 //
-// Few tokens (linear_rows_kernel): the weights' bytes bound the call.  Both
-// operands are decoded to bf16 (exact: E4M3 has four significant bits, the
+// Both operands are decoded to bf16 (exact: E4M3 has four significant bits, the
 // block scale is a power of two) and multiplied on the bf16 matrix cores,
-// whose products and sums are exact to float32; the FP8 matrix cores drop
-// bits below about 2^-16 of the largest product of a group (measured: 1.4e-5
-// of the sum's rms against 4e-8), and at these sizes their rate is not
-// needed.  9 x 6144 x 6144 10.5 us (39 MB, 3.7 TB/s), 72 x 4096 x 7168 16.9.
-// Many tokens (linear_tile_kernel): the FP8 matrix cores, tiles of up to
-// 256 x 256 staged through LDS.  4096 x 7168 x 7168 with bias and residual 200
-// us (2.1 PFLOP/s; weights and tokens from the caches 177), where the matrix
-// cores are busy 56 % of the time and their clock falls with random operands;
-// 288 x 7168 x 7168 34 us; 1001 x 2048 x 6144 27 us, 6 of them the pass over
-// the split sums.
+// whose products and sums are exact to float32.  The FP8 matrix cores, twice
+// as fast, keep the products of eight consecutive k to 13 bits below the
+// largest of them: 1.4e-5 of the sum's rms against 4e-8, and nothing of a
+// small product beside two large ones that cancel.  They are not used.
+// Few tokens (linear_rows_kernel): the weights' bytes bound the call.
+// 9 x 6144 x 6144 10.5 us (39 MB, 3.7 TB/s), 72 x 4096 x 7168 16.9.
+// Many tokens (linear_tile_kernel): tiles of up to 256 x 256 staged through LDS
+// as they are in memory; each wave decodes what it multiplies, between its
+// products.  4096 x 7168 x 7168 with bias and residual 343 us (1.23 PFLOP/s;
+// without them and from the caches 318, 1.32; a bf16 product of a library
+// reaches 1.26): bound by the matrix cores, at the clock that random operands
+// leave them, and the vector instructions beside them, and by the second
+// round's 192 tiles on 256 CUs (4096 x 8192 x 8192, two full rounds: 1.42
+// PFLOP/s).  288 x 7168 x 7168 54 us, 1001 x 2048 x 6144 37: one wave per SIMD,
+// whose products wait for its conversions.
 // Either may split the inner axis over workgroups that leave float32 sums in
 // the workspace for linear_finish_kernel.
 #include "lds_dma.h"
@@ -26,9 +30,7 @@
 namespace moe {
 namespace {
 
-__device__ inline i32x8_t operand(const uint4& lo, const uint4& hi) {
-    return i32x8_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-}
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 // v / (1 + exp(-v)); the hardware exponential and reciprocal (about 1 ulp each)
 __device__ inline float silu(float v) { return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
@@ -337,18 +339,21 @@ __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear
 // 8 whole rows: with the rows' pieces spread over the lanes in operand order
 // instead (16 rows x 64 bytes per load) every quarter of a wave touches 16
 // cache lines, and the loads alone took 1.55 us a chunk against 0.6.
-// Products: v_mfma_scale_f32_16x16x128_f8f6f4, lane (r, g) of an operand
-// holding the 16-byte pieces g and g + 4 of row r's 128 bytes and the scale of
-// block g (from registers alone, on random data: 3.79 PFLOP/s; the 32x32x64
-// shape, whose clock falls further, 3.28).
-template <int RQ, int TT, int STAGES>
+// Products: v_mfma_f32_32x32x16_bf16 (from registers alone, on random data:
+// 1.82 PFLOP/s, 1.80 with four conversions beside each, 1.51 with eight vector
+// instructions, two waves per SIMD).  Its operands take half the registers
+// of the 16x16x32 shape's at the same tile, which spilled (4096 x 7168 x
+// 7168: 525 us, 334 in this shape).
+constexpr int kStages = 2;  // chunks in LDS (three: no difference, 288 x 7168 x 7168 54.8 and 54.9 us)
+
+template <int RQ, int TT>
 struct TileSmem {
-    alignas(16) uint8_t a[STAGES][RQ][8192];
-    alignas(16) uint8_t b[STAGES][TT][4096];
+    alignas(16) uint8_t a[kStages][RQ][8192];
+    alignas(16) uint8_t b[kStages][TT][4096];
     struct {
         alignas(16) uint32_t a[RQ][kWave];
         alignas(16) uint32_t b[TT * 32];
-    } s[STAGES];  // the block scales
+    } s[kStages];  // the block scales
 };
 
 struct TileGrid {
@@ -363,24 +368,21 @@ __device__ inline void wait_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// Two waves per SIMD: with registers for one only the compiler keeps the sums
-// of 256 threads in accumulation registers and copies them around the second
-// phase (288 x 7168 x 7168: 39.2 us, 35.4 without).
-template <int ACT, bool MX, int RQ, int TT, int WR, int WT, int STAGES>
-__global__ void __launch_bounds__(WR * WT * kWave, 2) linear_tile_kernel(moe_mxfp8_linear_args a, TileGrid p) {
-    constexpr int kStages = STAGES, kWaves = WR * WT;
-    constexpr int Q = RQ / WR, NT = TT * 2 / WT;               // a wave's quads and 16-token tiles
-    constexpr int NG = 4 * Q;                                  // and 16-row groups
+template <int ACT, bool MX, int RQ, int TT, int WR, int WT>
+__global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_linear_args a, TileGrid p) {
+    constexpr int kWaves = WR * WT;
+    constexpr int Q = RQ / WR, NR = 2 * Q, NT = TT / WT;       // a wave's quads, 32-row and 32-token tiles
     constexpr int kA = RQ * 8 / kWaves, kB = TT * 4 / kWaves;  // 1 KB loads per wave and chunk
     constexpr int kS = (RQ + TT / 2) / kWaves;                 // and 256-byte loads of block scales
     static_assert(RQ * 8 % kWaves == 0 && TT * 4 % kWaves == 0 && (RQ + TT / 2) % kWaves == 0, "loads per wave");
     extern __shared__ uint8_t smem_raw[];
-    auto& sm = *reinterpret_cast<TileSmem<RQ, TT, kStages>*>(smem_raw);
+    auto& sm = *reinterpret_cast<TileSmem<RQ, TT>*>(smem_raw);
     const int w = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
     // Workgroups go round the eight XCDs; each XCD takes a run of the tiles,
     // numbered down bands of kBand token blocks, so that what its L2 holds of
-    // x and W serves several tiles (4096 x 7168 x 7168 from HBM: 206 us with
-    // the tiles dealt round, 200 with bands of 4, 203 of 2, 201 of 8)
+    // x and W serves several tiles (1024 x 7168 x 7168: 103 us, 108 with the
+    // tiles dealt round, 105 in bands of 2 or 8; 4096 x 7168 x 7168, bound by the
+    // matrix cores: 318, 319 and 318)
     const int tiles = p.row_blocks * p.tok_blocks, per_xcd = (tiles + 7) / 8;
     const int split = blockIdx.x / (8 * per_xcd), blk = blockIdx.x % (8 * per_xcd);
     const int id = blk % 8 * per_xcd + blk / 8;
@@ -447,133 +449,142 @@ __global__ void __launch_bounds__(WR * WT * kWave, 2) linear_tile_kernel(moe_mxf
         }
     };
     const int wr = w % WR, wt = w / WR;
-    f32x4_t acc[NG][NT];
+    f32x16_t acc[NR][NT];
 #pragma unroll
-    for (int i = 0; i < NG; i++)
+    for (int i = 0; i < NR; i++)
 #pragma unroll
-        for (int t = 0; t < NT; t++) acc[i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    const int a_at = (g & 1) * 1024 + (c + 16 * (g >> 1)) * 16;  // piece g; piece g + 4 is 512 bytes on
-    const int b_at = c * 128 + (g ^ (c / 2)) * 16;               // piece g; piece g + 4 is in slot ^ 4
-    i32x8_t A[NG], B[NT];
-    uint32_t sa[Q], sb[NT], sa_first = 0;  // sa_first: the next chunk's sa[0]
-    auto read_a = [&](int buf, auto i) {
-        const uint8_t* p = &sm.a[buf][wr * Q + i / 4][a_at + i % 4 * 2048];
-        A[i] = operand(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 512));
-        if constexpr (i % 4 == 0) {
-            const uint32_t v = sm.s[buf].a[wr * Q + i / 4][lane];
-            if constexpr (i == 0) sa_first = v;
-            else sa[i / 4] = v;
-        }
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int j = 0; j < 16; j++) acc[i][t][j] = 0.f;
+    // A chunk in eight steps z = 2 s + q of 16 k: lane (row l % 32, half = l / 32)
+    // of an operand holds bytes 8 q .. 8 q + 7 of the 16-byte piece 2 s + half of its
+    // row, of block s.  ar, br: the pieces of block s as they are in LDS, in
+    // place s % 2, the next block's in the other; Ad, Bd: decoded, the row tile
+    // of a product and the token tiles of a step, each beside the next one.
+    const int r32 = lane % 32, half = lane / 32;
+    const int a_at = lane / 16 % 2 * 2048 + half * 1024 + c * 16;  // block s is 256 s bytes on
+    const int a_byte = lane / 16 % 2 * 8;                       // its group's place in a word of scales
+    u32x4_t ar[2][NR], br[2][NT], Ad[2], Bd[2][NT];
+    uint32_t sa[2][Q], sb[NT], sb_next[NT];  // scale words: A's of a block, B's of a chunk
+    float a_scale[NR], b_scale[NT];          // of a block
+    auto read_a = [&](int buf, auto s, auto i) {
+        ar[s % 2][i] = *reinterpret_cast<const u32x4_t*>(&sm.a[buf][wr * Q + i / 2][a_at + i % 2 * 4096 + s * 256]);
+        if constexpr (i % 2 == 0) sa[s % 2][i / 2] = sm.s[buf].a[wr * Q + i / 2][c + 16 * s];
     };
-    auto read_b = [&](int buf, auto t) {
-        const int row = (wt * NT + t) * 16;
-        const uint8_t* p = &sm.b[buf][0][row * 128];
-        B[t] = operand(*reinterpret_cast<const uint4*>(p + b_at), *reinterpret_cast<const uint4*>(p + (b_at ^ 64)));
-        sb[t] = reinterpret_cast<const uint8_t*>(&sm.s[buf].b[row + c])[g];
+    auto read_b = [&](int buf, auto s, auto t) {
+        const int row = (wt * NT + t) * 32 + r32;
+        br[s % 2][t] = *reinterpret_cast<const u32x4_t*>(&sm.b[buf][0][row * 128 + ((2 * s + half) ^ (r32 / 2 % 8)) * 16]);
+        if constexpr (s == 0) sb_next[t] = sm.s[buf].b[row];
     };
-    // one product, after which also() goes out; the compiler keeps that order
-    auto product = [&](auto i, auto t, auto&& also) {
-        acc[i][t] = mfma_scaled<0, decltype(i)::value % 4, 0>(A[i], B[t], acc[i][t], sa[i / 4], sb[t]);
-        also();
-        __builtin_amdgcn_sched_barrier(0);
+    auto pair = [&](const u32x4_t& raw, auto q, auto e, float scale) {  // elements 2e, 2e + 1 of the step's eight
+        return __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * q.value + e.value / 2], scale, e.value % 2));
     };
-    // step n of `of` of something done in `count` parts
-    auto part = [&](auto n, auto of, auto count, auto&& f) {
-        constexpr int lo = decltype(n)::value * decltype(count)::value / decltype(of)::value;
-        constexpr int hi = (decltype(n)::value + 1) * decltype(count)::value / decltype(of)::value;
-        static_for<hi - lo>([&](auto j) { f(std::integral_constant<int, lo + decltype(j)::value>{}); });
+    auto decode_a = [&](auto s, auto q, auto i, auto e) {
+        if constexpr (q == 0 && e == 0)
+            a_scale[i] = e8m0_as_scale((sa[s % 2][i / 2] >> (a_byte + i % 2 * 16)) & 0xffu);
+        Ad[i % 2][e.value] = pair(ar[s % 2][i], q, e, a_scale[i]);
     };
-    // A chunk in two phases.  First the groups up to kFirst, one after the
-    // other, while the rest of A is read, a group a product; then this wave
-    // has read all of the chunk (lgkmcnt) and its loads of the next have
-    // landed (vmcnt), and past the barrier that holds for every wave.  Then
-    // the last groups, tile by tile: a tile of B done, its registers take the
-    // next chunk's, whose first kAheadA groups of A are read and the loads of the
-    // chunk kStages on (over this one) go out meanwhile.  A short first phase
-    // leaves B's reads more time (4 groups: 34.3 us with 1, 35.8 with 2, 37.0
-    // with 3, 288 x 7168 x 7168), a long one A's (8 groups: 200 us with 5, 201
-    // with 4, 208 with 3, 4096 x 7168 x 7168).
-    constexpr int kFirst = NG == 8 ? 5 : 1, kAheadA = NG == 8 ? 3 : 2, kLast = NG - kFirst;
-    const std::integral_constant<int, kLast * NT> in_second;
-    const std::integral_constant<int, kLoads> loads;
-    const std::integral_constant<int, kAheadA> ahead;
+    auto decode_b = [&](auto s, auto q, auto t, auto e) {
+        if constexpr (s == 0 && q == 0 && e == 0) sb[t] = sb_next[t];
+        if constexpr (q == 0 && e == 0) b_scale[t] = e8m0_as_scale((sb[t] >> (8 * s)) & 0xffu);
+        Bd[q][t][e.value] = pair(br[s % 2][t], q, e, b_scale[t]);
+    };
     const int n_chunks = k1 - k0;
+    const std::integral_constant<int, 0> zero;
     static_for<kStages>([&](auto st) {
         if (st < n_chunks) static_for<kLoads>([&](auto n) { issue(n, st); });
     });
     // the first chunk's loads have landed (those of the others may be in flight)
     if (n_chunks >= kStages) wait_barrier<(kStages - 1) * kLoads>();
     else wait_barrier<0>();
-    static_for<NT>([&](auto t) { read_b(0, t); });
-    static_for<kAheadA>([&](auto i) { read_a(0, i); });
     int buf = 0;
-    auto next = [&] { return buf + 1 == kStages ? 0 : buf + 1; };
-    auto first_phase = [&] {
-        sa[0] = sa_first;
-        static_for<kFirst>([&](auto i) {
-            static_for<NT>([&](auto t) {
-                product(i, t, [&] {
-                    constexpr int next_a = decltype(i)::value * NT + decltype(t)::value + kAheadA;
-                    if constexpr (next_a < NG) read_a(buf, std::integral_constant<int, next_a>{});
-                });
+    auto next = [&] { return 1 - buf; };
+    static_for<NT>([&](auto t) { read_b(0, zero, t); });
+    static_for<NR>([&](auto i) { read_a(0, zero, i); });
+    static_for<4 * NT>([&](auto n) {
+        decode_b(zero, zero, std::integral_constant<int, n / 4>{}, std::integral_constant<int, n % 4>{});
+    });
+    static_for<4>([&](auto e) { decode_a(zero, zero, zero, e); });
+    // One step: NR x NT products, and after each a part of what comes next, in
+    // this order (the compiler keeps it): the next row tile is decoded, the
+    // next step's token tiles, and in a block's first step the next block is
+    // read.  At step 6 this wave has read all of the chunk (lgkmcnt) and its
+    // loads of the next have landed (vmcnt); past the barrier that holds for
+    // every wave, and the loads of the chunk after that, over this one, go out.
+    constexpr int kSlots = NR * NT, kParts = 4 / NT;
+    auto step = [&](auto z, auto read_next, auto load_next) {
+        const std::integral_constant<int, z / 2> s;
+        const std::integral_constant<int, z % 2> q;
+        const std::integral_constant<int, (z + 1) % 8 / 2> s_next;  // of the next step
+        const std::integral_constant<int, 1 - z % 2> q_next;
+        constexpr bool more = z < 7 || decltype(read_next)::value, block = z < 6 || decltype(read_next)::value;
+        if constexpr (z == 6 && decltype(read_next)::value) wait_barrier<0>();
+        static_for<kSlots>([&](auto n) {
+            constexpr int i = n / NT, t = n % NT;
+            acc[i][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, Ad[i % 2]),
+                                                                __builtin_bit_cast(bf16x8_t, Bd[q][t]), acc[i][t], 0, 0, 0);
+            if constexpr (block && q == 0) {
+                const std::integral_constant<int, (z / 2 + 1) % 4> ahead;
+                const int from = z < 6 ? buf : next();
+                if constexpr (t == 0) read_a(from, ahead, std::integral_constant<int, i>{});
+                if constexpr (n < NT) read_b(from, ahead, n);
+            }
+            static_for<kParts>([&](auto j) {
+                const std::integral_constant<int, t * kParts + j> e;
+                if constexpr (i + 1 < NR) decode_a(s, q, std::integral_constant<int, i + 1>{}, e);
+                else if constexpr (more) decode_a(s_next, q_next, zero, e);
             });
+            if constexpr (more) {
+                constexpr int lo = n * 4 * NT / kSlots, hi = (n + 1) * 4 * NT / kSlots;
+                static_for<hi - lo>([&](auto j) {
+                    decode_b(s_next, q_next, std::integral_constant<int, (lo + j) / 4>{},
+                             std::integral_constant<int, (lo + j) % 4>{});
+                });
+            }
+            if constexpr (z >= 6 && decltype(load_next)::value) {
+                constexpr int at = (z - 6) * kSlots + n;
+                constexpr int lo = at * kLoads / (2 * kSlots), hi = (at + 1) * kLoads / (2 * kSlots);
+                static_for<hi - lo>([&](auto j) { issue(std::integral_constant<int, lo + j>{}, buf); });
+            }
+            __builtin_amdgcn_sched_barrier(0);
         });
     };
-    auto second_phase = [&](auto read_next, auto load_next) {
-        static_for<NT>([&](auto t) {
-            static_for<kLast>([&](auto j) {
-                constexpr int n = decltype(t)::value * kLast + decltype(j)::value;
-                product(std::integral_constant<int, kFirst + decltype(j)::value>{}, t, [&] {
-                    const std::integral_constant<int, n> at;
-                    if constexpr (decltype(load_next)::value)
-                        part(at, in_second, loads, [&](auto u) { issue(u, buf); });
-                    if constexpr (decltype(read_next)::value) {
-                        part(at, in_second, ahead, [&](auto u) { read_a(next(), u); });
-                        if constexpr (j == kLast - 1) read_b(next(), t);
-                    }
-                });
-            });
-        });
+    auto chunk = [&](auto read_next, auto load_next) {
+        static_for<8>([&](auto z) { step(z, read_next, load_next); });
+        buf = next();
     };
     int k = 0;
-    for (; k + kStages < n_chunks; k++) {
-        first_phase();
-        wait_barrier<(kStages - 2) * kLoads>();
-        second_phase(std::true_type{}, std::true_type{});
-        buf = next();
-    }
-    for (; k + 1 < n_chunks; k++) {  // nothing more to load
-        first_phase();
-        wait_barrier<0>();
-        second_phase(std::true_type{}, std::false_type{});
-        buf = next();
-    }
-    first_phase();
-    second_phase(std::false_type{}, std::false_type{});
+    for (; k + kStages < n_chunks; k++) chunk(std::true_type{}, std::true_type{});
+    for (; k + 1 < n_chunks; k++) chunk(std::true_type{}, std::false_type{});  // nothing more to load
+    chunk(std::false_type{}, std::false_type{});
 
-    // The sums go through this wave's own part of the LDS, two token tiles at
+    // The sums go through this wave's own part of the LDS, a token tile at
     // a time, to lanes that hold 8 consecutive columns of a token: rows of 16
     // lanes then read the residual and write the output in 256-byte runs.
     constexpr bool kGated = ACT == MOE_EPI_SILU_MUL;
     constexpr int kRow = 64 * Q + 4;                 // padded: 16-byte writes of 16 tokens cover all banks
     constexpr int kOcts = kGated ? 4 * Q : 8 * Q;    // output octets of a token
     constexpr int kItems = 32 * kOcts / kWave;       // per lane and token tile
-    static_assert(sizeof(TileSmem<RQ, TT, kStages>) >= kWaves * 32 * kRow * 4, "staging of the sums");
+    static_assert(sizeof(TileSmem<RQ, TT>) >= kWaves * 32 * kRow * 4, "staging of the sums");
     __syncthreads();  // every wave is done with the last chunk
     float(*mine)[kRow] = reinterpret_cast<float(*)[kRow]>(smem_raw + w * (32 * kRow * 4));
     const int64_t cols = kGated ? a.rows / 2 : a.rows;
     const int wq = q0 + wr * Q;                      // this wave's first quad
-    const int64_t tw = t0 + wt * NT * 16;            // and first token
-    auto stage = [&](auto t) {  // token tiles 2t, 2t + 1
+    const int64_t tw = t0 + wt * NT * 32;            // and first token
+    auto stage = [&](auto t) {
 #pragma unroll
-        for (int half = 0; half < 2; half++)
+        for (int i = 0; i < NR; i++)
 #pragma unroll
-            for (int i = 0; i < NG; i++)
-                *reinterpret_cast<f32x4_t*>(&mine[16 * half + c][16 * i + 4 * g]) = acc[i][2 * t + half];
+            for (int j = 0; j < 4; j++) {
+                const f32x16_t& v = acc[i][t];
+                *reinterpret_cast<f32x4_t*>(&mine[r32][32 * i + 8 * j + 4 * half]) =
+                    f32x4_t{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+            }
         __builtin_amdgcn_wave_barrier();
     };
     if (p.splits > 1) {
-        static_for<NT / 2>([&](auto t) {
+        static_for<NT>([&](auto t) {
             stage(t);
 #pragma unroll 2
             for (int n = 0; n < 32 * 8 * Q / kWave; n++) {
@@ -595,7 +606,7 @@ __global__ void __launch_bounds__(WR * WT * kWave, 2) linear_tile_kernel(moe_mxf
         add8(bias, a.bias + c0);
         if (kGated) add8(bias_u, a.bias + cols + c0);
     }
-    static_for<NT / 2>([&](auto t) {
+    static_for<NT>([&](auto t) {
         uint4 res[kItems];
 #pragma unroll
         for (int n = 0; n < kItems; n++) {
@@ -619,11 +630,10 @@ __global__ void __launch_bounds__(WR * WT * kWave, 2) linear_tile_kernel(moe_mxf
 }
 
 // ------------------------------------------------------------ the choice
-// Tokens of linear_rows_kernel: at 128 it is exact at about the tiles' speed
-// (128 x 4096 x 7168: 17.9 us, tiles 19.2; 128 x 7168 x 7168: 24.7 and 22.1).
+// Tokens of linear_rows_kernel (128 x 4096 x 7168: 18.9 us, tiles 22.8; 128 x
+// 7168 x 7168: 26.2 and 27.2; 192 x 7168 x 7168: 45.3 and 37.0)
 constexpr int kRowsMaxTok = 128, kRowsMostTok = 1024;
-constexpr int64_t kRowsMostWork = (int64_t)256 * 6144;  // workgroups times inner axis
-constexpr int kWideTiles = 160;    // from as many on 256 x 256 tiles
+constexpr int64_t kRowsMostWork = (int64_t)256 * 7168;  // workgroups times inner axis
 constexpr int kMaxSplits = 8;
 constexpr int kSplitTok = 8192;    // most tokens times splits (the workspace's bound)
 constexpr int kCus = 256;
@@ -633,7 +643,6 @@ struct LinearPlan {
     int G, NT, W;
     RowsGrid grid;
     bool wide;       // 256 x 256 tiles (else 128 x 128)
-    bool deep;       // 128 x 128 tiles staged three chunks deep (else two)
     TileGrid tile;
     int splits;
 };
@@ -644,30 +653,37 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
     const bool gated = activation == MOE_EPI_SILU_MUL;
     // linear_rows_kernel: few tokens, and more where its largest workgroups (64 rows x 64 tokens)
     // all run at once and the work is small, so that the tiles' launches of few
-    // workgroups would mostly wait (320 x 2048 x 2048: 8.2 us, tiles 13.6; 1024
-    // x 1024 x 1024: 8.0 and 10.6; 192 x 4096 x 7168: 19.4 and 20.0; past the
-    // bound 1024 x 1024 x 8192: 26.9 and 23.4)
+    // workgroups would mostly wait (320 x 2048 x 2048: 8.3 us, tiles 19.6; 1024
+    // x 1024 x 1024: 8.2 and 13.5; 256 x 4096 x 7168: 25.3 and 27.8; past the
+    // bound 256 x 4096 x 16384: 51.6 and 45.8; 1000 x 512 x 16384: 36.1 and 30.7)
     const int64_t most = rows / 64 * ((T + 63) / 64);
     p.rows = T <= kRowsMaxTok || (T <= kRowsMostTok && most <= kCus && most * inner <= kRowsMostWork);
     int64_t splits = 1;
     if (!p.rows) {
-        // 256 x 256 tiles move half the bytes per product, 128 x 128 leave fewer
-        // CUs idle (1536 x 7168 x 7168: 168 wide tiles 86 us, narrow ones 106;
-        // 1024 x 7168 x 7168: 112 wide tiles 82 us, narrow ones 66)
+        // 256 x 256 tiles, one per CU, decode each element for twice as many
+        // products; 128 x 128, two per CU, lose less to a round of few tiles.
+        // Wide where one round holds them and two of the narrow ones would
+        // not be enough for one, and where three quarters of the rounds' places
+        // are taken (K 4096, wide and narrow tiles, us: 140 wide tiles of 504
+        // narrow 88, 68; 144 of 576 83, 86; 308 176, 153; 364 177, 179; 392
+        // 181, 196; 532 279, 257; 616 279, 287; 784 378, 365; 1024 408, 463)
         const int64_t wide_blocks = (rows + 255) / 256 * ((T + 255) / 256);
-        p.wide = wide_blocks >= kWideTiles;
+        const int64_t narrow_blocks = (rows + 127) / 128 * ((T + 127) / 128);
+        p.wide = wide_blocks <= kCus ? narrow_blocks > 2 * kCus
+                                     : 4 * wide_blocks >= 3 * ((wide_blocks + kCus - 1) / kCus * kCus);
         const int n = p.wide ? 256 : 128;
         p.tile.row_blocks = (int)((rows + n - 1) / n);
         p.tile.tok_blocks = (int)((T + n - 1) / n);
-        // A 128-k chunk of a workgroup takes about 0.5 us, the pass over the
+        // A 128-k chunk of a workgroup takes about 0.9 us, the pass over the
         // split sums 2 us and 0.5 us per MB of them; the number of splits that
-        // leaves the least, of those that fit on the CUs (1024 x 2048 x 6144:
-        // 28.6 us in 2, 30.8 in 1; x 2048: 23.2 and 14.6).
+        // leaves the least, of those that fit on the CUs (1001 x 2048 x 6144:
+        // 36.6 us in 2, 46.1 in 1, 38.9 in 3; 512 x 2048 x 7168: 28.5 in 4,
+        // 34.2 in 2; 1024 x 2048 x 2048: 22.5 in 2, 21.2 in 1).
         const int64_t blocks = (int64_t)p.tile.row_blocks * p.tile.tok_blocks;
         const int64_t sums = T * rows * 4 / 1000000;  // MB
-        int64_t best = chunks;                        // in units of 0.5 us
+        int64_t best = 9 * chunks;                    // in units of 0.1 us
         for (int64_t n = 2; !p.wide && n <= kMaxSplits && n * blocks <= kCus && n * T <= kSplitTok; n++) {
-            const int64_t t = (chunks + n - 1) / n + 4 + n * sums;
+            const int64_t t = 9 * ((chunks + n - 1) / n) + 20 + 5 * n * sums;
             if (t < best) best = t, splits = n;
         }
     } else {
@@ -699,12 +715,6 @@ LinearPlan make_plan(int64_t T, int64_t rows, int64_t inner, int32_t activation,
     if (splits > chunks / 8) splits = chunks / 8;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;
-    // 128 x 128 tiles: up to one workgroup per CU the loads of two chunks
-    // are kept in flight (three stages, 101 KB of LDS); beyond that two
-    // workgroups per CU hide each other's waits (two stages).  512 x 4096 x
-    // 7168: 256 workgroups 31.6 us deep, 34.4 otherwise; 1024 x 7168 x 7168:
-    // 448 workgroups 76.7 deep, 66.3 otherwise.
-    p.deep = !p.rows && !p.wide && (int64_t)p.tile.row_blocks * p.tile.tok_blocks * splits <= kCus;
     const int per = (int)((chunks + splits - 1) / splits);
     p.splits = (chunks + per - 1) / per;
     p.grid.splits = p.tile.splits = p.splits;
@@ -720,10 +730,10 @@ hipError_t launch_rows(const moe_mxfp8_linear_args& a, const RowsGrid& p, hipStr
     return hipGetLastError();
 }
 
-template <int ACT, bool MX, int RQ, int TT, int WR, int WT, int STAGES>
+template <int ACT, bool MX, int RQ, int TT, int WR, int WT>
 hipError_t launch_tile(const moe_mxfp8_linear_args& a, const TileGrid& p, hipStream_t stream) {
-    constexpr int bytes = sizeof(TileSmem<RQ, TT, STAGES>);  // more than 64 KB: has to be asked for
-    const auto kernel = linear_tile_kernel<ACT, MX, RQ, TT, WR, WT, STAGES>;
+    constexpr int bytes = sizeof(TileSmem<RQ, TT>);  // more than 64 KB: has to be asked for
+    const auto kernel = linear_tile_kernel<ACT, MX, RQ, TT, WR, WT>;
     const hipError_t err =
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != hipSuccess) return err;
@@ -734,9 +744,7 @@ hipError_t launch_tile(const moe_mxfp8_linear_args& a, const TileGrid& p, hipStr
 
 template <int ACT, bool MX>
 hipError_t launch_tiles(const moe_mxfp8_linear_args& a, const LinearPlan& p, hipStream_t stream) {
-    if (p.wide) return launch_tile<ACT, MX, 4, 8, 2, 4, 2>(a, p.tile, stream);
-    return p.deep ? launch_tile<ACT, MX, 2, 4, 2, 2, 3>(a, p.tile, stream)
-                  : launch_tile<ACT, MX, 2, 4, 2, 2, 2>(a, p.tile, stream);
+    return p.wide ? launch_tile<ACT, MX, 4, 8, 2, 4>(a, p.tile, stream) : launch_tile<ACT, MX, 2, 4, 2, 2>(a, p.tile, stream);
 }
 
 }  // namespace
