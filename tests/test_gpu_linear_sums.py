@@ -8,9 +8,10 @@ eight consecutive k: a sum in fewer bits loses the small ones, which are the
 result.  Random sums: the residual is minus the rounded result, so that the
 output holds what a bf16 result hides.
 
-Sizes reach each form the call has: the few-token kernel, 128 x 128 tiles
-staged three and two deep, split sums and 256 x 256 tiles, each with several
-times the chunks (of 128 k) that are staged, odd and even counts."""
+FORMS: sizes of each form the call has (test_linear_plan_cpu.py holds them to
+it): the few-token kernel, 128 x 128 tiles with up to one workgroup per CU and
+with more, split sums, and 256 x 256 tiles, each with more chunks of 128 k
+than twice those in LDS, odd and even counts."""
 import numpy as np
 import pytest
 
@@ -20,11 +21,12 @@ from tests.test_gpu_mxfp8_linear import Case, encode
 
 pytestmark = pytest.mark.gpu
 
-# tokens, rows, inner
-FORMS = {"few": (100, 256, 1152), "few, above 128 tokens": (300, 512, 1152),
-         "deep": (1100, 256, 1152), "deep, whole tiles": (1152, 384, 1024), "shallow": (1300, 3328, 1152),
-         "shallow, even": (1409, 3200, 1024), "split": (1100, 192, 2176), "wide": (2600, 4096, 640),
-         "wide, even": (2561, 4160, 1024)}
+# name: (form, (tokens, rows, inner))
+FORMS = {"few tokens": ("rows", (100, 256, 1152)), "small product": ("rows", (300, 512, 1152)),
+         "narrow, a few": ("narrow", (1100, 256, 1152)), "narrow, whole tiles": ("narrow", (1152, 384, 1024)),
+         "narrow, two per CU": ("narrow", (1300, 3328, 1152)), "narrow, even": ("narrow", (1409, 3200, 1024)),
+         "split": ("narrow split", (1100, 192, 2176)), "wide": ("wide", (2600, 4096, 640)),
+         "wide, even": ("wide", (2561, 4160, 1024))}
 
 
 @pytest.fixture(scope="module")
@@ -59,7 +61,7 @@ def upload(c, M, x, w):
 
 @pytest.mark.parametrize("form", FORMS)
 def test_small_products_survive_large_ones(M, form):
-    T, rows, K = FORMS[form]
+    T, rows, K = FORMS[form][1]
     say(f"linear exact sums {form}: T={T} rows={rows} K={K}")
     x, w = planted(T, rows, K, T)
     assert ((np.abs(x) @ np.abs(w).T).max() + np.abs(x @ w.T).max()) / 2 < 2.0 ** 16
@@ -84,7 +86,7 @@ def test_error_of_random_sums(M, form):
     rounding to bf16 as much again of d: 2^-16 / 3.  K float32 additions of
     at most half a step of the running sum each, independent: sqrt(K) 2^-24 at
     most.  (The subtraction is exact.)"""
-    T, rows, K = FORMS[form]
+    T, rows, K = FORMS[form][1]
     say(f"linear error {form}: T={T} rows={rows} K={K}")
     c = Case(M, T, rows, K, seed=21)
     v = R.mx8_values(c.xc, c.xs) @ R.mx8_values(c.wc, c.ws).T
@@ -101,7 +103,7 @@ def test_error_of_random_sums(M, form):
 def test_float32_bound_everywhere(M, form, act, out):
     """The bound of a float32 sum (ops_reference.linear at few tokens), with
     bias and residual, for each form's steady loop."""
-    T, rows, K = FORMS[form]
+    T, rows, K = FORMS[form][1]
     say(f"linear float32 bound {form} {act}: T={T} rows={rows} K={K}")
     c = Case(M, T, rows, K, act, True, True, out, seed=22)
     o = c.run(M)
