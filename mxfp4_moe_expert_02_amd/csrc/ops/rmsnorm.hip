@@ -62,11 +62,25 @@ __device__ inline double sticky(double v) {
     return __builtin_bit_cast(double, (uint64_t)hi << 32);
 }
 
-// double -> bf16, one rounding: the sticky form holds every bit that
-// matters and float32's rounding to bf16 sees a tie only where there is one
-__device__ inline float to_f32_odd(double v) { return (float)sticky(v); }
-
 constexpr int kNormPiece = 8;
+
+// double -> the float32 whose rounding to bf16 is the double's: the sticky
+// form holds every bit that matters, and float32's rounding to bf16 sees a tie
+// only where there is one.  Below float32's normal range its steps (2^-149)
+// lose the sticky bit: there v is rounded to bf16's subnormals (steps of
+// 2^-133) in 64 bits.
+__device__ inline void round_once(const double (&v)[kNormPiece], float (&o)[kNormPiece]) {
+    bool small = false;
+#pragma unroll
+    for (int e = 0; e < kNormPiece; e++) {
+        o[e] = (float)sticky(v[e]);
+        small |= fabsf(o[e]) < 0x1p-126f;
+    }
+    if (small)
+#pragma unroll
+        for (int e = 0; e < kNormPiece; e++)
+            if (fabs(v[e]) < 0x1p-126) o[e] = (float)(rint(v[e] * 0x1p133) * 0x1p-133);
+}
 
 // WPR: waves per row, 1 (four rows per workgroup of 256 threads) or more
 // (one row per workgroup); NP: pieces of 8 elements per thread.
@@ -113,8 +127,9 @@ rmsnorm_kernel(moe_rmsnorm_args a) {
         for (int p = 0; p < NP; p++) {
             const int i = p * kThreads + tid;
             float o[kNormPiece];
+            // s is a whole multiple of 2^-149: float32's below its normal range
 #pragma unroll
-            for (int e = 0; e < kNormPiece; e++) o[e] = sizeof(R) == 2 ? to_f32_odd(s[p][e]) : (float)s[p][e];
+            for (int e = 0; e < kNormPiece; e++) o[e] = (float)(sizeof(R) == 2 ? sticky(s[p][e]) : s[p][e]);
             if (i < pieces) store_piece<kNormPiece>(ro + i * kNormPiece, o);
         }
     }
@@ -137,8 +152,7 @@ rmsnorm_kernel(moe_rmsnorm_args a) {
         for (int e = 0; e < kNormPiece; e++) n[e] = s[p][e] * (double)wv[p][e] * rinv;
         if (y && live) {
             float o[kNormPiece];
-#pragma unroll
-            for (int e = 0; e < kNormPiece; e++) o[e] = to_f32_odd(n[e]);
+            round_once(n, o);
             store_piece<kNormPiece>(y + i * kNormPiece, o);
         }
         if (!a.codes) continue;

@@ -1,0 +1,38 @@
+"""Calls at the ends of the operators' ranges."""
+import numpy as np
+import pytest
+
+from tests import ops_reference as R
+from tests.gpu_common import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def M():
+    import mxfp4_moe_expert_02_amd as M
+    return M
+
+
+@pytest.mark.parametrize("H", [512, 2048, 16384])
+def test_norm_results_below_the_normal_range_are_rounded_once(M, H):
+    """y just beside the middle of two of bf16's subnormals (steps of 2^-133), by
+    less than float32's subnormals can tell (2^-149): the nearer one, not the
+    even one.  x = 1/2 (1 + d) in every column and eps = 1 - x^2 make the norm's
+    factor 1 to 2^-51; n = w (1 + d) / 2."""
+    import torch
+    say(f"rmsnorm subnormal y H={H}")
+    for d in (2.0 ** -22, -2.0 ** -22, 0.0):
+        x = 0.5 * (1 + d)
+        k = np.arange(H) % 200
+        w = (2 * k + 1) * 2.0 ** -133 * np.where(np.arange(H) % 3 == 0, -1.0, 1.0)   # n = (k + 1/2) steps
+        xt, wt = R.tensor(np.full((3, H), x), "f32"), R.tensor(w, "f32")
+        assert np.array_equal(R.values(wt), w) and np.array_equal(R.values(xt), np.full((3, H), x))
+        y = torch.full((3, H), 7.0, dtype=torch.bfloat16, device="cuda")
+        M.moe_rmsnorm(xt, wt, 1.0 - x * x, y=y)
+        _, n = R.rmsnorm(R.values(xt), None, w, 1.0 - x * x)
+        if d:
+            assert np.array_equal(R.values(y), R.bf16_rne(n))
+        else:  # on the middle itself, or 2^-51 beside it
+            err = np.abs(n) * (H + 8) * 2.0 ** -53
+            R.assert_between(R.values(y), R.bf16_rne(n - err), R.bf16_rne(n + err), "y")
