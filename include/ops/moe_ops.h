@@ -205,7 +205,7 @@ int moe_dispatch(const moe_dispatch_args* args, void* stream);
  *   drows[pos[t, j], :] = weights[t, j] * dout[t, :]
  *   dweights[t, j]      = <dout[t, :], rows[pos[t, j], :]>, 0 without a position
  * drows rows that no slot points to are left as they were; either output
- * may be NULL (not both). */
+ * may be NULL (not both, unless num_rows is 0). */
 typedef struct moe_combine_args {
     const void* rows;         /* [num_rows, hidden], rows_dtype (backward: NULL if dweights is) */
     int64_t rows_stride;

@@ -139,7 +139,8 @@ int check_combine(moe_combine_args* a, bool backward) {
     if (!backward) {
         if (!a->out || (!a->rows && a->num_rows > 0)) return MOE_E_NULL;
     } else {
-        if (!a->dout || (!a->drows && !a->dweights)) return MOE_E_NULL;
+        // without rows an empty drows may well be null
+        if (!a->dout || (!a->drows && !a->dweights && a->num_rows > 0)) return MOE_E_NULL;
         if (a->dweights && !a->rows && a->num_rows > 0) return MOE_E_NULL;
         if (a->drows && a->drows == a->rows && a->drows_stride != a->rows_stride) return MOE_E_SHAPE;
     }

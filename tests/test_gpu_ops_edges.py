@@ -36,3 +36,23 @@ def test_norm_results_below_the_normal_range_are_rounded_once(M, H):
         else:  # on the middle itself, or 2^-51 beside it
             err = np.abs(n) * (H + 8) * 2.0 ** -53
             R.assert_between(R.values(y), R.bf16_rne(n - err), R.bf16_rne(n + err), "y")
+
+
+def test_combine_gradient_without_rows(M):
+    """No row is held here: every position is elsewhere, and there is nothing to
+    write but zeros for the weights."""
+    import torch
+    say("combine backward without rows")
+    T, k, H = 5, 3, 64
+    dout, w = torch.randn(T, H, device="cuda"), torch.rand(T, k, device="cuda")
+    pos = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    pos[2, 1] = 4                                # past the rows
+    for dt in (torch.float32, torch.bfloat16):
+        rows, drows = torch.empty(0, H, dtype=dt, device="cuda"), torch.empty(0, H, dtype=dt, device="cuda")
+        assert M.moe_combine_backward(dout, rows, w, pos, drows, None) == M.MOE_OK
+        dw = torch.full((T, k), 3.0, device="cuda")
+        M.moe_combine_backward(dout, rows, w, pos, drows, dw)
+        out = torch.full((T, H), 3.0, device="cuda")
+        M.moe_combine(rows, w, pos, out)
+        torch.cuda.synchronize()
+        assert not dw.any() and not out.any()
