@@ -33,8 +33,14 @@ namespace {
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
-// v / (1 + exp(-v)); the hardware exponential and reciprocal (about 1 ulp each)
-__device__ inline float silu(float v) { return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
+// v / (1 + exp(-v)), relative error up to (8 + |v|) 2^-23 (the exponential's
+// argument is rounded).  Below -64 the 1 does not count, and from -87 on
+// exp(-v) and then its reciprocal leave float32's normal range while v exp(v)
+// is inside it: taken there in two halves.
+__device__ inline float silu(float v) {
+    const float h = __expf(0.5f * v);
+    return v < -64.f ? v * h * h : v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+}
 
 // v / 2 * (1 + erf(v / sqrt 2)) = v / 2 * erfc(-v / sqrt 2): erfc keeps the
 // relative precision of the left tail that 1 + erf loses.  For a >= 0,

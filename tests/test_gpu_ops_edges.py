@@ -56,3 +56,27 @@ def test_combine_gradient_without_rows(M):
         M.moe_combine(rows, w, pos, out)
         torch.cuda.synchronize()
         assert not dw.any() and not out.any()
+
+
+@pytest.mark.parametrize("T", [3, 200])
+@pytest.mark.parametrize("act", ["silu", "silu_mul"])
+def test_silu_of_large_arguments(M, T, act):
+    """SiLU over the whole range where its result is a float32, through the bias
+    (W is zero): v / (1 + exp(-v)) is normal down to v = -91.8, where exp(-v)
+    has left float32's range."""
+    import torch
+    say(f"linear {act} of large arguments T={T}")
+    rows, K = 1024, 128
+    n = rows // 2 if act == "silu_mul" else rows
+    v = np.concatenate([np.linspace(-103.9, 104, n - 6), [-91.5, -88.75, -88.5, -87.4, -1e4, 1e4]]).astype(np.float32)
+    v = v.astype(np.float64)
+    u = np.full(n, 1.0)
+    bias = np.concatenate([v, u]) if act == "silu_mul" else v
+    z = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")
+    out = torch.full((T, n), 3.0, dtype=torch.bfloat16, device="cuda")
+    M.moe_mxfp8_linear(z(T, K), z(T, K // 32), z(rows, K), z(rows, K // 32), out=out, bias=R.tensor(bias, "f32"),
+                       activation=M.MOE_EPI_SILU if act == "silu" else M.MOE_EPI_SILU_MUL)
+    a = R.silu(v)
+    err = (8 + np.abs(v)) * R.STEP * np.abs(a) + 2.0 ** -149
+    lo, hi = R.bf16_rne(a - err), R.bf16_rne(a + err)
+    R.assert_between(R.values(out), np.broadcast_to(lo, (T, n)), np.broadcast_to(hi, (T, n)), "silu")
