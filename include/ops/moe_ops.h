@@ -102,7 +102,9 @@ int moe_rmsnorm(const moe_rmsnorm_args* args, void* stream);
  *
  * Products and sums are float32's at every size (about 1e-7 of the sum's
  * rms); how the sum is ordered goes by the sizes alone.  Values of x and W
- * outside float32's normal range may count as zero or infinity.
+ * outside float32's normal range may count as zero or infinity, and GELU's
+ * results below it are zero.  SiLU's relative error is up to (8 + |v|) 2^-23,
+ * GELU's up to (16 + 2 v^2) 2^-23.
  *
  * x [num_tokens, inner] and W [rows, inner] in MXFP8; W in the MXFP8 tile
  * layout of moe_mxfp8_prepack, with gate_up_pairs = 1 for MOE_EPI_SILU_MUL
