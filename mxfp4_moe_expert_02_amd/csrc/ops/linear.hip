@@ -276,12 +276,16 @@ __global__ void __launch_bounds__(W * kWave) linear_rows_kernel(moe_mxfp8_linear
         static_for<D>([&](auto d) {
             if (d < n) load(wb[d], seg + d, d);
         });
-        // In the steady loop every load is unconditional (a skipped one makes
-        // the compiler wait for all); the last chunks have none to skip.
+        // The wait below counts loads: the next D - 1 chunks' may stay in flight.
+        // The weights are ordinary loads, though, for which the compiler waits
+        // by itself, and after the conditional loads above it waits for all of
+        // them once per D chunks (vmcnt(0) in the compiled loop of all eleven
+        // shapes): what was issued last is then in flight for one chunk's
+        // products only.
         int i = 0;
         for (; i + 2 * D <= n; i += D)
             static_for<D>([&](auto d) {
-                // this chunk has landed, the next D - 1 may be in flight
+                // this chunk has landed
                 asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * kLoads) : "memory");
                 multiply(wb[d], i + d, d);
                 load(wb[d], seg + i + D + d, d);
