@@ -8,10 +8,14 @@
 //   3. workgroups of a few tokens each count the slots of their chunk that
 //      come before them, place their own, and copy their rows: a token's
 //      row is read once and written to its places.
-// Up to kSumChunks chunks step 3 sums the chunks' counts itself (a launch of
-// one workgroup costs 12 us against 2 for the sums: 32768 slots, 128
-// experts), and up to kOneLaunchSlots slots it counts the slots themselves:
-// the call is then one launch without workspace.
+// With few counts step 3 sums them itself, every workgroup all of them, in
+// place of step 2's launch of one workgroup; by their number times a chunk's
+// workgroups (8 places a token, rows of 1024, summed and scanned, us: 16384
+// slots of 256 experts 19.6, 21.6; 32768 of 128 27.6, 32.1; 65536 of 64 43.5,
+// 51.6; beyond the bound 16384 of 512 24.1, 22.2; 65536 of 128 57.6, 52.4, of
+// 1024 272, 58; one place, order alone: 16384 of 64 13.4, 14.2, of 256 18.8,
+// 15.4).  Up to kOneLaunchSlots slots it counts the slots themselves: the
+// call is then one launch without workspace.
 // Positions are integers counted in slot order: the result does not depend
 // on which workgroup runs when.
 // Bound by the rows' bytes, each read once and written to its k places: 4096
@@ -27,7 +31,7 @@ constexpr int kThreads = 256;
 constexpr int kChunkSlots = 1024;
 constexpr int kMaxChunks = 2048;
 constexpr int kOneLaunchSlots = 4096;
-constexpr int kSumChunks = 64;
+constexpr int64_t kSumWork = 1 << 19;  // counts times workgroups of a chunk
 constexpr int kMaxTokSlots = 64;  // slots of one gather workgroup, at least one token
 
 struct Plan {
@@ -40,7 +44,7 @@ struct Plan {
 // where place_rows_kernel gets the positions before its own chunk from
 enum class First { kSlots, kCounts, kScanned };
 
-Plan make_plan(int64_t T, int k) {
+Plan make_plan(int64_t T, int E, int k) {
     Plan p;
     const int64_t S = T * k;
     p.one = S <= kOneLaunchSlots;
@@ -48,13 +52,13 @@ Plan make_plan(int64_t T, int k) {
     if (slots < kChunkSlots) slots = kChunkSlots;
     p.chunk_tok = p.one ? (int)T : (int)((slots + k - 1) / k);
     p.chunks = (int)((T + p.chunk_tok - 1) / p.chunk_tok);
-    p.sums = !p.one && p.chunks <= kSumChunks;
     // one token a workgroup (4096 tokens to 8 places each: 115 us, 117 with
     // four, 121 with eight); of long chunks, which every workgroup recounts, a
     // fair share
     p.wg_tok = p.chunk_tok / 256 > 1 ? p.chunk_tok / 256 : 1;
     if (p.wg_tok * k > kMaxTokSlots) p.wg_tok = kMaxTokSlots / k;
     p.wgs = (p.chunk_tok + p.wg_tok - 1) / p.wg_tok;
+    p.sums = !p.one && (int64_t)p.chunks * E * p.wgs <= kSumWork;
     return p;
 }
 
@@ -175,7 +179,7 @@ place_rows_kernel(moe_dispatch_args a, Plan p, const int32_t* first, int64_t row
     if (tid < n) own[tid] = a.ids[t0 * k + tid];
     __syncthreads();
     if (FROM == First::kCounts) {
-        const int cells = p.chunks * E;  // at most kSumChunks * kMaxExperts
+        const int cells = p.chunks * E;
         for (int i0 = tid; i0 < cells; i0 += 8 * kThreads) {
             int h[8];
 #pragma unroll
@@ -259,7 +263,7 @@ int copy_bytes(const void* p, const void* q, int64_t row, int64_t stride) {
 
 int64_t dispatch_workspace(int64_t T, int64_t E, int32_t k) {
     if (T == 0) return 0;
-    const Plan p = make_plan(T, k);
+    const Plan p = make_plan(T, (int)E, k);
     return p.one ? 0 : (int64_t)p.chunks * E * 4;
 }
 
@@ -269,7 +273,7 @@ hipError_t launch_dispatch(const moe_dispatch_args& a, hipStream_t stream) {
         no_slots_kernel<<<1, kThreads, 0, stream>>>(E, a.counts, a.offsets);
         return hipGetLastError();
     }
-    const Plan p = make_plan(a.num_tokens, k);
+    const Plan p = make_plan(a.num_tokens, E, k);
     const int64_t esize = a.dtype == MOE_DT_BF16 ? 2 : a.dtype == MOE_DT_F32 ? 4 : 1;
     const int64_t row = a.hidden * esize, xrow = a.x_stride * esize;
     const int vec = copy_bytes(a.x, a.rows, row, xrow);

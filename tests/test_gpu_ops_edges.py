@@ -4,6 +4,7 @@ import pytest
 
 from tests import ops_reference as R
 from tests.gpu_common import say
+from tests.test_gpu_dispatch_combine import _dispatch, _ids, _x
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,11 @@ def test_silu_of_large_arguments(M, T, act):
     err = (8 + np.abs(v)) * R.STEP * np.abs(a) + 2.0 ** -149
     lo, hi = R.bf16_rne(a - err), R.bf16_rne(a + err)
     R.assert_between(R.values(out), np.broadcast_to(lo, (T, n)), np.broadcast_to(hi, (T, n)), "silu")
+
+
+@pytest.mark.parametrize("T,k,E", [(4096, 8, 128), (4224, 8, 128), (4096, 8, 129), (8192, 8, 1024), (16384, 1, 128),
+                                   (16385, 1, 128), (2048, 32, 64), (70_000, 1, 7), (20_000, 4, 1024)])
+def test_dispatch_on_both_sides_of_its_choice(M, T, k, E):
+    """Counts summed by each workgroup, and scanned in a launch of their own."""
+    say(f"dispatch T={T} k={k} E={E}")
+    _dispatch(M, _x(T, 8, "bf16", T), _ids(T, k, E, T + k), E)
