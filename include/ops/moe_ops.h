@@ -138,8 +138,9 @@ typedef struct moe_mxfp8_linear_args {
     int32_t reserved;         /* 0 */
 } moe_mxfp8_linear_args;
 
-/* Bytes of workspace a call of these sizes needs (0: none), or a negative
- * status for sizes moe_mxfp8_linear refuses. */
+/* Bytes of workspace a call of these sizes needs (0: none), the same for
+ * both kinds of output (MXFP8's need, asked of a bf16 call as well), or a
+ * negative status for sizes moe_mxfp8_linear refuses. */
 int64_t moe_mxfp8_linear_workspace(int64_t num_tokens, int64_t rows, int64_t inner, int32_t activation);
 
 /* Exactly one of out and out_codes (with out_scales) must be given.  All

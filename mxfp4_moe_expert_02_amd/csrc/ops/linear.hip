@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(WR * WT * kWave) linear_tile_kernel(moe_mxfp8_
     static_assert(RQ * 8 % kWaves == 0 && TT * 4 % kWaves == 0 && (RQ + TT / 2) % kWaves == 0, "loads per wave");
     extern __shared__ uint8_t smem_raw[];
     auto& sm = *reinterpret_cast<TileSmem<RQ, TT>*>(smem_raw);
-    const int w = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
+    const int w = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, c = lane % 16;
     // Workgroups go round the eight XCDs; each XCD takes a run of the tiles,
     // numbered down bands of kBand token blocks, so that what its L2 holds of
     // x and W serves several tiles (1024 x 7168 x 7168: 103 us, 108 with the
