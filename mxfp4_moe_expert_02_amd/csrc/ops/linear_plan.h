@@ -51,11 +51,12 @@ inline LinearPlan linear_plan(int64_t T, int64_t rows, int64_t inner, int32_t ac
     if (!p.rows) {
         // 256 x 256 tiles, one per CU, decode each element for twice as many
         // products; 128 x 128, two per CU, lose less to a round of few tiles.
-        // Wide where one round holds them and two of the narrow ones would
-        // not be enough for one, and where three quarters of the rounds' places
-        // are taken (K 4096, wide and narrow tiles, us: 140 wide tiles of 504
-        // narrow 88, 68; 144 of 576 83, 86; 308 176, 153; 364 177, 179; 392
-        // 181, 196; 532 279, 257; 616 279, 287; 784 378, 365; 1024 408, 463)
+        // Up to one round of wide tiles: wide if the narrow ones would not run
+        // all at once; beyond it: wide if they fill three quarters of the
+        // places of their rounds (K 4096, wide and narrow, us: 140 wide tiles,
+        // 504 narrow 88, 68; 144, 576 83, 86; 308, 1232 176, 153; 364, 1456 177,
+        // 179; 392, 1568 181, 196; 532, 2128 279, 257; 616, 2464 279, 287; 784,
+        // 3136 378, 365; 1024, 4096 408, 463)
         const int64_t wide_blocks = (rows + 255) / 256 * ((T + 255) / 256);
         const int64_t narrow_blocks = (rows + 127) / 128 * ((T + 127) / 128);
         p.wide = wide_blocks <= kCus ? narrow_blocks > 2 * kCus
