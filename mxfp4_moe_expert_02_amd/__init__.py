@@ -3,9 +3,11 @@
 The layer itself is hand-written HIP in ``csrc/`` behind the C ABI of
 ``include/moe_mxfp4.h``, built into ``libmoe_mxfp4.so`` by ``build.py``.
 ``_lib`` is the ctypes binding (same names as the C ABI); ``_ops`` that of the
-operators around the layer (``include/ops/moe_ops.h``); ``layer`` builds a
-device-resident synthetic layer for tests and benchmarks.
+operators around the layer (``include/ops/moe_ops.h``), ``_attention`` that of
+the key/value cache and the attention over it (``include/ops/moe_attention.h``);
+``layer`` builds a device-resident synthetic layer for tests and benchmarks.
 """
+from ._attention import moe_kv_read, moe_kv_write, moe_tree_attention, moe_tree_attention_workspace
 from ._lib import (MOE_ACT_BF16, MOE_ACT_MXFP8, MOE_DT_BF16, MOE_DT_F32, MOE_DT_I32, MOE_DT_U8,
                    MOE_E_ALIGN, MOE_E_DTYPE, MOE_E_HIP, MOE_E_LIMIT,
                    MOE_E_NOT_INIT, MOE_E_NULL, MOE_E_OPTION, MOE_E_SHAPE, MOE_E_TOKENS, MOE_E_TOPK,
