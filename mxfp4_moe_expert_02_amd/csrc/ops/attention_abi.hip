@@ -84,7 +84,7 @@ int check_attention(moe_tree_attention_args* a) {
         misaligned(a->workspace, 16) || a->q_stride % 8 || a->out_stride % 8)
         return MOE_E_ALIGN;
     const moe::AttentionPlan plan = moe::attention_plan(T, B, a->num_heads, a->cache.kv_heads, a->cache.head_dim);
-    if (moe::attention_most_units(T, B, a->num_heads, a->cache.kv_heads, plan.row_tiles,
+    if (moe::attention_most_units(T, B, a->num_heads, a->cache.kv_heads, plan.rows,
                                   a->max_pages * a->cache.page_size) > kMaxUnits)
         return MOE_E_LIMIT;
     if (!a->workspace) return MOE_E_NULL;

@@ -7,13 +7,13 @@
 
 namespace moe {
 
-// Positions that a workgroup takes at once (32 of each of its 4 waves)
+// Positions that a workgroup takes at once
 constexpr int kAttnUnit = 128;
 
 struct AttentionPlan {
-    int row_tiles;       // 16-row tiles of a workgroup: rows are (drafted token, head of a kv head)
-    int groups;          // workgroups
-    int64_t part_floats; // floats of one partial result (16 * row_tiles rows of head_dim, and two statistics a row)
+    int rows;            // of a workgroup: (drafted token, query head of a key/value head)
+    int groups;          // workgroups, a multiple of 8
+    int64_t part_floats; // floats of one partial result: the rows' elements, and two statistics a row
     int64_t bytes;       // of the workspace: two partial results per workgroup
 };
 
@@ -22,18 +22,18 @@ inline AttentionPlan attention_plan(int64_t T, int64_t B, int64_t heads, int64_t
     if (T <= 0 || B <= 0) return p;
     // the rows of an average sequence (the lengths are the device's)
     const int64_t rows = (T + B - 1) / B * (heads / kv_heads);
-    p.row_tiles = rows <= 16 ? 1 : rows <= 32 || D == 256 ? 2 : 4;
-    p.groups = p.row_tiles == 4 ? 256 : 512;
-    p.part_floats = (int64_t)16 * p.row_tiles * (D + 2);
+    p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    p.groups = D == 256 || p.rows >= 64 ? 256 : p.rows == 16 ? 768 : 512;
+    p.part_floats = p.rows * (D + 2);
     p.bytes = p.groups * 2 * p.part_floats * 4;
     return p;
 }
 
 // Units of all sequences together at most, T tokens of B sequences, a table
 // of `positions` each
-inline int64_t attention_most_units(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int row_tiles,
+inline int64_t attention_most_units(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int rows,
                                     int64_t positions) {
-    const int64_t tiles = T * (heads / kv_heads) / (16 * row_tiles) + B;
+    const int64_t tiles = T * (heads / kv_heads) / rows + B;
     return tiles * kv_heads * ((positions + kAttnUnit - 1) / kAttnUnit);
 }
 

@@ -32,7 +32,7 @@
 namespace moe {
 namespace {
 
-constexpr int kAttnThreads = 256, kAttnWaves = 4;
+constexpr int kJoinWaves = 4;
 constexpr float kAttnSlack = 8.f;  // powers of two that a score may pass m by
 
 struct AttnArgs {
@@ -137,13 +137,35 @@ __device__ inline int sequence_at(const AttnArgs& p, int u, bool token, int* bas
 
 // ------------------------------------------------------------------ one wave
 
-// 32 positions' keys and values of one head as they lie in the cache: for
-// position 16 t + c a quarter of the elements and its scales
+// How 32 positions of one head go through a wave.  In the cache a position's
+// codes are D contiguous bytes.  A load takes whole lines: kLanes lanes of 16
+// bytes a position, kKeys positions at a time, kLoads times (16 lanes on 16
+// lines, as the matrix cores' operands would have them, cost 64 cycles a load
+// in place of 16).  K lies in LDS as it came, its 16-byte pieces dealt so that
+// the 16 positions of an operand read are in different banks; V lies there in
+// bf16, 16 bytes between its positions for the same reason.
+template <int D>
+struct Tile {
+    static constexpr int kLanes = D / 16, kKeys = kWave / kLanes, kLoads = 32 / kKeys;
+    static constexpr int kValueRow = 2 * D + 16;           // bytes of a position's values in LDS
+    static constexpr int kValues = 32 * kValueRow;         // V, then
+    static constexpr int kCodes = 32 * D;                  // K, then
+    static constexpr int kScales = 2 * 32 * (D / 32);      // both's scales
+    static constexpr int kBytes = kValues + kCodes + kScales;
+    // where piece `piece` of position `key`'s codes is
+    __device__ static int code_at(int key, int piece) {
+        return key * D + (piece ^ (key / (256 / D) % kLanes)) * 16;
+    }
+};
+
+// 32 positions' keys and values as loaded: lane l has piece l % kLanes of
+// position kKeys i + l / kLanes; the scales of position l % 32, lanes 0 .. 31
+// of K, the others of V
 template <int D>
 struct Raw {
-    uint4 k[2][D / 64], v[2][D / 64];
-    uint32_t ks[2], vs[2];
-    bool ok[2];  // the 16 positions' page is one of the cache's
+    u32x4_t k[Tile<D>::kLoads], v[Tile<D>::kLoads];
+    uint64_t scales;  // D / 32 bytes
+    bool ok[2];    // the page of the first 16 positions and of the others is one of the cache's
 };
 
 // page numbers of positions p0 .. p0+15 and p0+16 .. p0+31 (-1: none)
@@ -153,43 +175,33 @@ __device__ inline void page_numbers(const AttnArgs& p, const int32_t* table, int
 }
 
 template <int D>
-__device__ inline uint32_t load_scales(const uint8_t* s, int c, int g) {
-    if constexpr (D == 64) return s[c * 2 + g / 2];
-    else if constexpr (D == 128) return s[c * 4 + g];
-    else return *reinterpret_cast<const uint16_t*>(s + c * 8 + 2 * g);
-}
-
-template <int D>
-__device__ inline void load_raw(const AttnArgs& p, int h, int p0, const int (&page)[2], int c, int g, Raw<D>& r) {
+__device__ inline void load_raw(const AttnArgs& p, int h, int p0, const int (&page)[2], Raw<D>& r) {
+    using T = Tile<D>;
     const moe_kv_cache& q = p.a.cache;
+    const uint32_t lane = threadIdx.x % kWave;
+    int64_t at[2];
+    int row[2];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
         const int number = uniform(page[t]);
         r.ok[t] = (uint32_t)number < (uint32_t)q.num_pages;
-        const int64_t at = r.ok[t] ? number : 0;
-        const int row = h * q.page_size + ((p0 + 16 * t) & (q.page_size - 1));
-        const int64_t code = at * q.codes_page_stride + (int64_t)row * D;
-        const int64_t scale = at * q.scales_page_stride + (int64_t)row * (D / 32);
-        const uint8_t* k = q.k_codes + code + c * D + g * (D / 4);
-        const uint8_t* v = q.v_codes + code + c * D + g * (D / 4);
-#pragma unroll
-        for (int i = 0; i < D / 64; i++) r.k[t][i] = reinterpret_cast<const uint4*>(k)[i];
-#pragma unroll
-        for (int i = 0; i < D / 64; i++) r.v[t][i] = reinterpret_cast<const uint4*>(v)[i];
-        r.ks[t] = load_scales<D>(q.k_scales + scale, c, g);
-        r.vs[t] = load_scales<D>(q.v_scales + scale, c, g);
+        at[t] = r.ok[t] ? number : 0;
+        row[t] = h * q.page_size + ((p0 + 16 * t) & (q.page_size - 1));
     }
-}
-
-// the scale of a lane's elements 8 j .. 8 j + 7
-template <int D>
-__device__ inline float scale_of(uint32_t s, int j) {
-    return e8m0_as_scale(D == 256 && j >= 4 ? s >> 8 : D == 256 ? s & 0xffu : s);
-}
-template <int D>
-__device__ inline bf16x8_t decode_piece(const uint4 (&x)[D / 64], uint32_t s, int j) {
-    const uint4& w = x[j / 2];
-    return j % 2 ? decode8_e4m3(w.z, w.w, scale_of<D>(s, j)) : decode8_e4m3(w.x, w.y, scale_of<D>(s, j));
+#pragma unroll
+    for (int i = 0; i < T::kLoads; i++) {
+        const int t = i * T::kKeys / 16;
+        const int64_t code = at[t] * q.codes_page_stride + (int64_t)(row[t] + i * T::kKeys % 16) * D;
+        r.k[i] = *reinterpret_cast<const u32x4_t*>(q.k_codes + code + lane * 16);
+        r.v[i] = *reinterpret_cast<const u32x4_t*>(q.v_codes + code + lane * 16);
+    }
+    const int t = lane / 16 % 2;
+    const uint8_t* s = (lane < 32 ? q.k_scales : q.v_scales) +
+                       ((t ? at[1] : at[0]) * q.scales_page_stride + (int64_t)(t ? row[1] : row[0]) * (D / 32)) +
+                       lane % 16 * (D / 32);
+    if constexpr (D == 64) r.scales = *reinterpret_cast<const uint16_t*>(s);
+    else if constexpr (D == 128) r.scales = *reinterpret_cast<const uint32_t*>(s);
+    else r.scales = *reinterpret_cast<const uint64_t*>(s);
 }
 
 __device__ inline f32x4_t mfma(const bf16x8_t& a, const bf16x8_t& b, const f32x4_t& c) {
@@ -227,25 +239,17 @@ __device__ inline uint32_t seen_bits(const AttnArgs& p, const Seq& s, int node, 
     return seen & (ok0 ? ~0u : 0xffff0000u) & (ok1 ? ~0u : 0xffffu);
 }
 
-// LDS bytes of a position's values: its elements in bf16, and 32 bytes so
-// that neighbouring positions start 8 banks apart
-constexpr int value_bytes(int D) { return 2 * D + 32; }
-
 // A word of two bf16 values: 2^127 for each that is no finite number, else zero
 __device__ inline uint32_t specials(uint32_t w) {
     return ((w & 0x7f80u) == 0x7f80u ? 0x7f00u : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0x7f000000u : 0u);
 }
 
-// whether a lane's values hold one that is no finite number: a NaN code or
-// scale, or a scale (2^127 or 2^126) that can take one out of range
-template <int D>
-__device__ inline bool has_specials(const uint4 (&x)[D / 64], uint32_t s) {
-    uint32_t nan = 0;  // the high bit of each byte whose lower seven are all set
-#pragma unroll
-    for (int i = 0; i < D / 64; i++)
-        nan |= ((x[i].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].y & 0x7f7f7f7fu) + 0x01010101u) |
-               ((x[i].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].w & 0x7f7f7f7fu) + 0x01010101u);
-    return (nan & 0x80808080u) || (s & 0xffu) >= 246u || s >> 8 >= 246u;
+// whether 16 values hold one that is no finite number: a NaN code or scale, or
+// a scale that can take one out of range
+__device__ inline bool has_specials(const u32x4_t& x, uint32_t s) {
+    const uint32_t nan = ((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) |
+                         ((x.z & 0x7f7f7f7fu) + 0x01010101u) | ((x.w & 0x7f7f7f7fu) + 0x01010101u);
+    return (nan & 0x80808080u) || s >= 246u;
 }
 
 template <int D, int R>
@@ -260,38 +264,46 @@ struct Wave {
 template <int D, int R, typename Ahead>
 __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R], const bf16x8_t (&q)[R][D / 32],
                             int p0, Raw<D>& raw, uint8_t* lds, Wave<D, R>& w, Ahead&& ahead) {
+    using T = Tile<D>;
     const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
-    uint8_t* mine = lds + c * value_bytes(D) + g * (D / 2);
+    const int key = lane / T::kLanes, piece = lane % T::kLanes;  // of a load
+    uint8_t *codes = lds + T::kValues, *scales = codes + T::kCodes;
+    // K and the scales as they are
+    if constexpr (D == 64) *reinterpret_cast<uint16_t*>(scales + lane * 2) = (uint16_t)raw.scales;
+    else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(scales + lane * 4) = (uint32_t)raw.scales;
+    else *reinterpret_cast<uint64_t*>(scales + lane * 8) = raw.scales;
+#pragma unroll
+    for (int i = 0; i < T::kLoads; i++)
+        *reinterpret_cast<u32x4_t*>(codes + T::code_at(T::kKeys * i + key, piece)) = raw.k[i];
+    wave_order();
+    // V in bf16
+    uint32_t vs[T::kLoads];
+#pragma unroll
+    for (int i = 0; i < T::kLoads; i++) vs[i] = scales[(32 + T::kKeys * i + key) * (D / 32) + piece / 2];
+    const bool ok0 = raw.ok[0], ok1 = raw.ok[1];
     // whether some of them are drafted ones or none at all; else all rows see all
-    const bool special = p0 + 32 > s.L || !raw.ok[0] || !raw.ok[1];
+    const bool special = p0 + 32 > s.L || !ok0 || !ok1;
     bool odd = false;  // a drafted token's value is no number
     if (special) {
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-            if (!(p0 + 16 * t + c < s.len && raw.ok[t])) {  // nothing is there
-#pragma unroll
-                for (int i = 0; i < D / 64; i++) raw.v[t][i] = make_uint4(0, 0, 0, 0);
-                raw.vs[t] = 0;
+        for (int i = 0; i < T::kLoads; i++) {
+            if (!(p0 + T::kKeys * i + key < s.len && (i * T::kKeys / 16 ? ok1 : ok0))) {  // nothing is there
+                raw.v[i] = u32x4_t{0, 0, 0, 0};
+                vs[i] = 0;
             }
-            odd |= has_specials<D>(raw.v[t], raw.vs[t]);
+            odd |= has_specials(raw.v[i], vs[i]);
         }
         odd = __any(odd);
     }
+    uint8_t* mine = lds + key * T::kValueRow + piece * 32;
 #pragma unroll
-    for (int t = 0; t < 2; t++)
-#pragma unroll
-        for (int j = 0; j < D / 32; j++)
-            *reinterpret_cast<bf16x8_t*>(mine + t * 16 * value_bytes(D) + 16 * j) =
-                decode_piece<D>(raw.v[t], raw.vs[t], j);
-    wave_order();
-    const bool ok0 = raw.ok[0], ok1 = raw.ok[1];
-    Raw<D> now;
-#pragma unroll
-    for (int t = 0; t < 2; t++) {
-        now.ks[t] = raw.ks[t];
-#pragma unroll
-        for (int i = 0; i < D / 64; i++) now.k[t][i] = raw.k[t][i];
+    for (int i = 0; i < T::kLoads; i++) {
+        const float f = e8m0_as_scale(vs[i]);
+        bf16x8_t* at = reinterpret_cast<bf16x8_t*>(mine + T::kKeys * i * T::kValueRow);
+        at[0] = decode8_e4m3(raw.v[i].x, raw.v[i].y, f);
+        at[1] = decode8_e4m3(raw.v[i].z, raw.v[i].w, f);
     }
+    wave_order();
     ahead();
 
     f32x4_t st[2][R];
@@ -299,13 +311,36 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
     for (int t = 0; t < 2; t++) {
 #pragma unroll
         for (int r = 0; r < R; r++) st[t][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        // lane (c, g): quarter g of position 16 t + c
+        uint32_t ks = 0;
+        if constexpr (D == 64) ks = scales[(16 * t + c) * 2 + g / 2];
+        else if constexpr (D == 128) ks = scales[(16 * t + c) * 4 + g];
+        else ks = *reinterpret_cast<const uint16_t*>(scales + (16 * t + c) * 8 + 2 * g);
 #pragma unroll
-        for (int j = 0; j < D / 32; j++) {
-            const bf16x8_t k = decode_piece<D>(now.k[t], now.ks[t], j);
+        for (int j = 0; j < D / 64; j++) {
+            const uint4 x = *reinterpret_cast<const uint4*>(codes + T::code_at(16 * t + c, g * (D / 64) + j));
+            const float f = e8m0_as_scale(D == 256 ? (j < 2 ? ks & 0xffu : ks >> 8) : ks);
+            const bf16x8_t k0 = decode8_e4m3(x.x, x.y, f), k1 = decode8_e4m3(x.z, x.w, f);
 #pragma unroll
-            for (int r = 0; r < R; r++) st[t][r] = mfma(k, q[r][j], st[t][r]);
+            for (int r = 0; r < R; r++) st[t][r] = mfma(k0, q[r][2 * j], st[t][r]);
+#pragma unroll
+            for (int r = 0; r < R; r++) st[t][r] = mfma(k1, q[r][2 * j + 1], st[t][r]);
         }
     }
+    typedef __attribute__((address_space(3))) s16x4_t lds4_t;
+    const uint8_t* column = lds + (4 * g + c / 4) * T::kValueRow + (c % 4) * 8;
+    auto value = [&](int d) {
+        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t*)(column + 32 * d));
+        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t*)(column + 16 * T::kValueRow + 32 * d));
+        const s16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        return __builtin_bit_cast(bf16x8_t, v);
+    };
+    // the first of the product's operands are on their way before the softmax
+    constexpr int kAhead = 4;
+    bf16x8_t vt[kAhead];
+#pragma unroll
+    for (int d = 0; d < kAhead; d++) vt[d] = value(d);
+    __builtin_amdgcn_sched_barrier(0);
     uint32_t seen[R];
     if (special) {
 #pragma unroll
@@ -359,14 +394,6 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
 #pragma unroll
     for (int r = 0; r < R; r++) w.sum[r] = mfma(ones, pt[r], w.sum[r]);
 
-    typedef __attribute__((address_space(3))) s16x4_t lds4_t;
-    const uint8_t* column = lds + (4 * g + c / 4) * value_bytes(D) + (c % 4) * 8;
-    auto value = [&](int d) {
-        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t*)(column + 32 * d));
-        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t*)(column + 16 * value_bytes(D) + 32 * d));
-        const s16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        return __builtin_bit_cast(bf16x8_t, v);
-    };
     if (odd) {
         // A value that is no number makes one of what sees it, and of
         // nothing else.  2^127 in its place is multiplied with 2^127 where
@@ -391,20 +418,22 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
         }
         wave_order();
 #pragma unroll 1
-        for (int i = 0; i < 2 * (D / 32); i++) {
-            uint4* at = reinterpret_cast<uint4*>(mine + i / (D / 32) * 16 * value_bytes(D) + i % (D / 32) * 16);
+        for (int i = 0; i < 2 * T::kLoads; i++) {
+            uint4* at = reinterpret_cast<uint4*>(mine + i / 2 * T::kKeys * T::kValueRow + i % 2 * 16);
             const uint4 v = *at;
             auto clean = [](uint32_t x) { const uint32_t n = specials(x);
                 return x & ~((n & 0x4000u ? 0xffffu : 0u) | (n & 0x40000000u ? 0xffff0000u : 0u)); };
             *at = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
         }
         wave_order();
+#pragma unroll
+        for (int d = 0; d < kAhead; d++) vt[d] = value(d);
     }
 #pragma unroll
     for (int d = 0; d < D / 16; d++) {
-        const bf16x8_t v = value(d);
 #pragma unroll
-        for (int r = 0; r < R; r++) w.o[r][d] = mfma(v, pt[r], w.o[r][d]);
+        for (int r = 0; r < R; r++) w.o[r][d] = mfma(vt[d % kAhead], pt[r], w.o[r][d]);
+        if (d + kAhead < D / 16) vt[d % kAhead] = value(d + kAhead);
     }
     wave_order();
 }
@@ -412,23 +441,31 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
 // the statistic of rows without a position is -infinity: their weight is 0
 __device__ inline float reference(float m) { return m == minus_inf() ? 0.f : m; }
 
-// waves per SIMD that the registers of a variant leave room for
-constexpr int waves_per_simd(int D, int R) { return D * R <= 128 ? 3 : D * R <= 256 ? 2 : 1; }
+// A workgroup's shape: WR groups of 16 R rows times WK runs of positions, a
+// wave each.
+template <int D_, int R_, int WR_, int WK_>
+struct Shape {
+    static constexpr int D = D_, R = R_, WR = WR_, WK = WK_;
+    static constexpr int kRows = 16 * R * WR, kWaves = WR * WK, kThreads = kWave * kWaves;
+    // a wave's 32 positions; at the end the waves' results, 16 rows of each
+    static constexpr int kTile = Tile<D>::kBytes, kResult = 16 * (D + 4) * 4;
+    static constexpr int kLds = kWaves * (kTile > kResult ? kTile : kResult);
+    // waves per SIMD that the registers leave room for
+    static constexpr int kPerSimd = D == 256 ? 1 : D * R <= 128 ? 3 : 2;
+};
 
-template <int D, int R>
-constexpr int lds_bytes() {
-    const int values = kAttnWaves * 32 * value_bytes(D), joined = kAttnWaves * 16 * (D + 4) * 4;
-    return values > joined ? values : joined;
-}
-
-template <int D, int R>
-__global__ void __launch_bounds__(kAttnThreads, waves_per_simd(D, R)) tree_attention_kernel(AttnArgs p) {
-    constexpr int ROWS = 16 * R;
-    __shared__ __align__(16) uint8_t buf[lds_bytes<D, R>()];
-    __shared__ float s_m[kAttnWaves][ROWS], s_sum[kAttnWaves][16];
+template <typename S>
+__global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kernel(AttnArgs p) {
+    constexpr int D = S::D, R = S::R, WR = S::WR, WK = S::WK, ROWS = S::kRows;
+    __shared__ __align__(16) uint8_t buf[S::kLds];
+    __shared__ float s_m[WK][ROWS], s_sum[S::kWaves][16];
     const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave), c = lane % 16, g = lane / 16;
+    const int wr = wave / WK, wk = wave % WK;
+    // Workgroups are dealt round the 8 XCDs; each XCD takes a run of the line, so
+    // that the row tiles of a head, which read the same positions, share its L2
+    const int group = (int)blockIdx.x % 8 * (p.groups / 8) + (int)blockIdx.x / 8;
     const Line line = line_of<ROWS>(p);
-    int u = uniform((int)blockIdx.x * line.per);
+    int u = uniform(group * line.per);
     const int end = uniform(min(u + line.per, line.total));
     if (u >= end) return;
     int base = 0;
@@ -451,7 +488,7 @@ __global__ void __launch_bounds__(kAttnThreads, waves_per_simd(D, R)) tree_atten
         Wave<D, R> w;
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            const int row = row0 + 16 * r + c, live = row < rows;
+            const int row = row0 + 16 * (R * wr + r) + c, live = row < rows;
             node[r] = (live ? row : rows - 1) / p.G;
             const uint16_t* src = (const uint16_t*)p.a.q + (int64_t)(s.first + node[r]) * p.a.q_stride +
                                   (h * p.G + (live ? row % p.G : 0)) * D + g * (D / 4);
@@ -467,67 +504,70 @@ __global__ void __launch_bounds__(kAttnThreads, waves_per_simd(D, R)) tree_atten
             w.mc[r] = 0.f;
             w.pass[r] = minus_inf();
         }
-        // positions that some row of the tile may see
+        // positions that some row of the wave may see
         int stop = s.len;
-        if (!p.a.mask) stop = min(stop, s.L + (min(row0 + ROWS, rows) - 1) / p.G + 1);
-        stop = min(stop, u1 * kAttnUnit);
+        if (!p.a.mask) stop = min(stop, s.L + (min(row0 + 16 * R * (wr + 1), rows) - 1) / p.G + 1);
+        stop = row0 + 16 * R * wr < rows ? min(stop, u1 * kAttnUnit) : 0;
         const int32_t* table = p.a.block_table + (int64_t)b * p.a.block_table_stride;
-        int p0 = u0 * kAttnUnit + 32 * wave;
+        int p0 = u0 * kAttnUnit + 32 * wk;
         if (p0 < stop) {
             Raw<D> raw;
             int page[2];
             page_numbers(p, table, p0, s.len, page);
-            load_raw<D>(p, h, p0, page, c, g, raw);
-            page_numbers(p, table, p0 + kAttnUnit, s.len, page);
-            uint8_t* lds = buf + wave * 32 * value_bytes(D);
-            for (; p0 < stop; p0 += kAttnUnit) {
+            load_raw<D>(p, h, p0, page, raw);
+            page_numbers(p, table, p0 + 32 * WK, s.len, page);
+            uint8_t* lds = buf + wave * S::kTile;
+            for (; p0 < stop; p0 += 32 * WK) {
                 auto ahead = [&] {
-                    const int next = p0 + kAttnUnit;
+                    const int next = p0 + 32 * WK;
                     if (next < stop) {
-                        load_raw<D>(p, h, next, page, c, g, raw);
-                        page_numbers(p, table, next + kAttnUnit, s.len, page);
+                        load_raw<D>(p, h, next, page, raw);
+                        page_numbers(p, table, next + 32 * WK, s.len, page);
                     }
                 };
                 step<D, R>(p, s, node, q, p0, raw, lds, w, ahead);
             }
         }
 
-        // the four waves' results joined
+        // the results of the waves of a row group joined, 16 rows of each group at a time
         if (g == 0)
 #pragma unroll
-            for (int r = 0; r < R; r++) s_m[wave][16 * r + c] = w.m[r] == minus_inf() ? minus_inf() : w.mc[r];
+            for (int r = 0; r < R; r++)
+                s_m[wk][16 * (R * wr + r) + c] = w.m[r] == minus_inf() ? minus_inf() : w.mc[r];
         __syncthreads();
         auto top_of = [&](int row) {
             float m = s_m[0][row];
 #pragma unroll
-            for (int i = 1; i < kAttnWaves; i++) m = fmaxf(m, s_m[i][row]);
+            for (int i = 1; i < WK; i++) m = fmaxf(m, s_m[i][row]);
             return m;
         };
         const bool whole = u0 == 0 && u1 == units;
-        float* part = (float*)p.a.workspace + (2 * (int64_t)blockIdx.x + (u0 ? 0 : 1)) * p.part_floats;
+        float* part = (float*)p.a.workspace + (2 * (int64_t)group + (u0 ? 0 : 1)) * p.part_floats;
         float* joined = reinterpret_cast<float*>(buf);
+        constexpr int kPiece = D * 16 * WR / S::kThreads, kPieces = D / kPiece;  // of a row: elements of a thread, threads
 #pragma unroll
         for (int r = 0; r < R; r++) {
             const float f = __builtin_amdgcn_exp2f((w.m[r] == minus_inf() ? minus_inf() : w.mc[r]) -
-                                                   reference(top_of(16 * r + c)));
+                                                   reference(top_of(16 * (R * wr + r) + c)));
             float* mine = joined + (wave * 16 + c) * (D + 4) + 4 * g;
 #pragma unroll
             for (int d = 0; d < D / 16; d++)
                 *reinterpret_cast<f32x4_t*>(mine + 16 * d) = w.o[r][d] * f;
             if (g == 0) s_sum[wave][c] = w.sum[r][0] * f;
             __syncthreads();
-            const int row = tid / 16, d0 = tid % 16 * (D / 16), at = 16 * r + row;
-            float v[D / 16] = {}, sum = 0.f;
+            const int og = tid / (16 * kPieces), orow = tid / kPieces % 16, d0 = tid % kPieces * kPiece;
+            const int at = 16 * (R * og + r) + orow;
+            float v[kPiece] = {}, sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < kAttnWaves; i++) {
-                sum += s_sum[i][row];
+            for (int i = 0; i < WK; i++) {
+                sum += s_sum[og * WK + i][orow];
 #pragma unroll
-                for (int d = 0; d < D / 16; d++) v[d] += joined[(i * 16 + row) * (D + 4) + d0 + d];
+                for (int d = 0; d < kPiece; d++) v[d] += joined[((og * WK + i) * 16 + orow) * (D + 4) + d0 + d];
             }
             if (!whole) {
                 float* dst = part + at * D + d0;
 #pragma unroll
-                for (int d = 0; d < D / 16; d++) dst[d] = v[d];
+                for (int d = 0; d < kPiece; d++) dst[d] = v[d];
                 if (d0 == 0) {
                     part[ROWS * D + 2 * at] = top_of(at);
                     part[ROWS * D + 2 * at + 1] = sum;
@@ -537,7 +577,7 @@ __global__ void __launch_bounds__(kAttnThreads, waves_per_simd(D, R)) tree_atten
                 uint16_t* dst = (uint16_t*)p.a.out + (int64_t)(s.first + (row0 + at) / p.G) * p.a.out_stride +
                                 (h * p.G + (row0 + at) % p.G) * D + d0;
 #pragma unroll
-                for (int d = 0; d < D / 16; d += 4) {
+                for (int d = 0; d < kPiece; d += 4) {
                     const float o[4] = {v[d] * inv, v[d + 1] * inv, v[d + 2] * inv, v[d + 3] * inv};
                     store_piece<4>(dst + d, o);
                 }
@@ -550,11 +590,11 @@ __global__ void __launch_bounds__(kAttnThreads, waves_per_simd(D, R)) tree_atten
 
 // One wave per row: the parts of a row tile that several workgroups did, in
 // their order.  A part's weight is 2^(its reference - the largest).
-template <int D, int R>
-__global__ void __launch_bounds__(kAttnThreads) tree_attention_join_kernel(AttnArgs p) {
-    constexpr int ROWS = 16 * R, N = D / kWave;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinWaves * kWave) tree_attention_join_kernel(AttnArgs p) {
+    constexpr int N = D / kWave;
     const int lane = threadIdx.x % kWave;
-    const int idx = uniform((int)blockIdx.x * kAttnWaves + (int)threadIdx.x / kWave);
+    const int idx = uniform((int)blockIdx.x * kJoinWaves + (int)threadIdx.x / kWave);
     if (idx >= p.T * p.a.num_heads) return;
     const int token = idx / p.a.num_heads, head = idx % p.a.num_heads;
     const Line line = line_of<ROWS>(p);
@@ -598,14 +638,25 @@ __global__ void __launch_bounds__(kAttnThreads) tree_attention_join_kernel(AttnA
     for (int e = 0; e < N; e++) dst[e] = f32_to_bf16_rne(v[e] * inv);
 }
 
-template <int D, int R>
-hipError_t launch_rows(const AttnArgs& p, hipStream_t stream) {
-    tree_attention_kernel<D, R><<<p.groups, kAttnThreads, 0, stream>>>(p);
+template <int D, int R, int WR, int WK>
+hipError_t launch_shape(const AttnArgs& p, hipStream_t stream) {
+    using S = Shape<D, R, WR, WK>;
+    tree_attention_kernel<S><<<p.groups, S::kThreads, 0, stream>>>(p);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const unsigned blocks = ((unsigned)p.T * p.a.num_heads + kAttnWaves - 1) / kAttnWaves;
-    tree_attention_join_kernel<D, R><<<blocks, kAttnThreads, 0, stream>>>(p);
+    const unsigned blocks = ((unsigned)p.T * p.a.num_heads + kJoinWaves - 1) / kJoinWaves;
+    tree_attention_join_kernel<D, S::kRows><<<blocks, kJoinWaves * kWave, 0, stream>>>(p);
     return hipGetLastError();
+}
+
+template <int D, int W>  // W: waves of the larger shapes
+hipError_t launch_rows(const AttnArgs& p, int rows, hipStream_t stream) {
+    switch (rows) {
+        case 16: return launch_shape<D, 1, 1, 4>(p, stream);
+        case 32: return launch_shape<D, 2, 1, 4>(p, stream);
+        case 64: return launch_shape<D, 2, 2, W / 2>(p, stream);
+        default: return launch_shape<D, 2, 4, W / 4>(p, stream);
+    }
 }
 
 }  // namespace
@@ -623,17 +674,10 @@ hipError_t launch_tree_attention(const moe_tree_attention_args& a, hipStream_t s
     p.groups = plan.groups;
     p.c = a.scale * 1.44269504088896340736f;
     p.part_floats = plan.part_floats;
-    const int R = plan.row_tiles;
     switch (a.cache.head_dim) {
-        case 64:
-            return R == 1   ? launch_rows<64, 1>(p, stream)
-                   : R == 2 ? launch_rows<64, 2>(p, stream)
-                            : launch_rows<64, 4>(p, stream);
-        case 128:
-            return R == 1   ? launch_rows<128, 1>(p, stream)
-                   : R == 2 ? launch_rows<128, 2>(p, stream)
-                            : launch_rows<128, 4>(p, stream);
-        default: return R == 1 ? launch_rows<256, 1>(p, stream) : launch_rows<256, 2>(p, stream);
+        case 64: return launch_rows<64, 8>(p, plan.rows, stream);
+        case 128: return launch_rows<128, 8>(p, plan.rows, stream);
+        default: return launch_rows<256, 4>(p, plan.rows, stream);
     }
 }
 
