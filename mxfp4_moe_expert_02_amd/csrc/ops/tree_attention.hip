@@ -58,9 +58,10 @@ struct Seq {
 };
 __device__ inline Seq read_seq(const AttnArgs& p, int b) {
     Seq s;
-    s.first = p.a.token_offsets[b];
-    s.n = p.a.token_offsets[b + 1] - s.first;
-    s.L = min(max(p.a.context_lens[b], 0), p.capacity);
+    const int first = p.a.token_offsets[b], next = p.a.token_offsets[b + 1], L = p.a.context_lens[b];
+    s.first = first;
+    s.n = next - first;
+    s.L = min(max(L, 0), p.capacity);
     s.len = min(s.L + s.n, p.capacity);
     return s;
 }
@@ -69,6 +70,10 @@ __device__ inline int tiles_of(const AttnArgs& p, const Seq& s) {
     return (s.n * p.G + ROWS - 1) / ROWS;
 }
 __device__ inline int units_of(const Seq& s) { return max(1, (s.len + kAttnUnit - 1) / kAttnUnit); }
+template <int ROWS>
+__device__ inline int weight_of(const AttnArgs& p, const Seq& s) {  // its units, of all heads and row tiles
+    return s.n ? tiles_of<ROWS>(p, s) * units_of(s) * p.a.cache.kv_heads : 0;
+}
 
 // inclusive sums over the wave's lanes
 __device__ inline int wave_scan(int v) {
@@ -83,125 +88,140 @@ __device__ inline int wave_scan(int v) {
 
 // All units in one line: sequence by sequence, in each its heads, in each head
 // its row tiles, in each of them its units.  Every wave works the line out
-// for itself, 64 sequences at a time (the lengths are the device's).
+// for itself, 64 sequences at a time, one a lane (the lengths are the device's).
 struct Line {
     int total;  // units; 0 if the offsets are not ascending in 0 .. T
     int per;    // units of a workgroup
+    // the last 64 sequences: the lane's, its units and those up to its end
+    Seq s;
+    int w, incl;
 };
-// units of a lane's sequence b
 template <int ROWS>
-__device__ inline int weight_of(const AttnArgs& p, int b, bool* bad) {
-    if (b >= p.B) return 0;
-    const Seq s = read_seq(p, b);
-    if (s.first < 0 || s.first > p.T || s.n < 0 || s.n > p.T - s.first) {
+__device__ inline void line_part(const AttnArgs& p, int b, Line* l, bool* bad) {
+    l->s = read_seq(p, min(b, p.B - 1));
+    if (l->s.first < 0 || l->s.first > p.T || l->s.n < 0 || l->s.n > p.T - l->s.first) {
         *bad = true;
-        return 0;
+        l->s.n = 0;
     }
-    return s.n ? tiles_of<ROWS>(p, s) * units_of(s) * p.a.cache.kv_heads : 0;
+    l->w = b < p.B ? weight_of<ROWS>(p, l->s) : 0;
+    l->incl = wave_scan(l->w);
 }
 template <int ROWS>
 __device__ inline Line line_of(const AttnArgs& p) {
     const int lane = threadIdx.x % kWave;
-    int total = 0;
-    bool bad = false;
-    for (int b0 = 0; b0 < p.B; b0 += kWave)
-        total += __builtin_amdgcn_readlane(wave_scan(weight_of<ROWS>(p, b0 + lane, &bad)), kWave - 1);
     Line l;
-    l.total = __any(bad) ? 0 : total;
+    l.total = 0;
+    bool bad = false;
+    for (int b0 = 0; b0 < p.B; b0 += kWave) {
+        line_part<ROWS>(p, b0 + lane, &l, &bad);
+        l.total += __builtin_amdgcn_readlane(l.incl, kWave - 1);
+    }
+    if (__any(bad)) l.total = 0;
     l.per = max(1, (l.total + p.groups - 1) / p.groups);
     return l;
 }
 
 // The sequence of unit u (u < total), or with `token` of token u (-1: none),
-// and the units before it.  After line_of found the offsets in order.
+// and the units before it; for a line that has units.
 template <int ROWS>
-__device__ inline int sequence_at(const AttnArgs& p, int u, bool token, int* base) {
+__device__ inline int sequence_at(const AttnArgs& p, int u, bool token, Line* l, Seq* s, int* base) {
     const int lane = threadIdx.x % kWave;
     int before = 0;
     for (int b0 = 0; b0 < p.B; b0 += kWave) {
         bool bad = false;
-        const int b = b0 + lane, w = weight_of<ROWS>(p, b, &bad), incl = wave_scan(w);
-        const int total = __builtin_amdgcn_readlane(incl, kWave - 1);
-        const bool mine = token ? b < p.B && p.a.token_offsets[b] <= u && u < p.a.token_offsets[b + 1]
-                                : u - before < incl && u - before >= incl - w;
+        if (p.B > kWave) line_part<ROWS>(p, b0 + lane, l, &bad);  // else line_of left it
+        const bool mine = token ? b0 + lane < p.B && l->s.first <= u && u - l->s.first < l->s.n
+                                : u - before < l->incl && u - before >= l->incl - l->w;
         const uint64_t at = __ballot(mine);
         if (at) {
-            const int l = __builtin_ctzll(at);
-            *base = before + __builtin_amdgcn_readlane(incl - w, l);
-            return b0 + l;
+            const int i = __builtin_ctzll(at);
+            *base = before + __builtin_amdgcn_readlane(l->incl - l->w, i);
+            s->first = __builtin_amdgcn_readlane(l->s.first, i);
+            s->n = __builtin_amdgcn_readlane(l->s.n, i);
+            s->L = __builtin_amdgcn_readlane(l->s.L, i);
+            s->len = __builtin_amdgcn_readlane(l->s.len, i);
+            return b0 + i;
         }
-        before += total;
+        before += __builtin_amdgcn_readlane(l->incl, kWave - 1);
     }
     return -1;
 }
 
 // ------------------------------------------------------------------ one wave
 
-// How 32 positions of one head go through a wave.  In the cache a position's
-// codes are D contiguous bytes.  A load takes whole lines: kLanes lanes of 16
-// bytes a position, kKeys positions at a time, kLoads times (16 lanes on 16
-// lines, as the matrix cores' operands would have them, cost 64 cycles a load
-// in place of 16).  K lies in LDS as it came, its 16-byte pieces dealt so that
+// How 32 positions of one head (a tile) go to the waves of a row group's
+// workgroup.  In the cache a position's codes are D contiguous bytes.  A load
+// takes whole lines: kLanes lanes of 16 bytes a position, kKeys positions at a
+// time (16 lanes on 16 lines, as the matrix cores' operands would have them,
+// cost 64 cycles a load in place of 16); the WR waves that share the tile take
+// kLoads / WR each.  K lies in LDS as it came, its 16-byte pieces dealt so that
 // the 16 positions of an operand read are in different banks; V lies there in
 // bf16, 16 bytes between its positions for the same reason.
 template <int D>
 struct Tile {
+    typedef typename std::conditional<D == 64, uint16_t, typename std::conditional<D == 128, uint32_t, uint64_t>::type>::type scales_t;
     static constexpr int kLanes = D / 16, kKeys = kWave / kLanes, kLoads = 32 / kKeys;
-    static constexpr int kValueRow = 2 * D + 16;           // bytes of a position's values in LDS
-    static constexpr int kValues = 32 * kValueRow;         // V, then
-    static constexpr int kCodes = 32 * D;                  // K, then
-    static constexpr int kScales = 2 * 32 * (D / 32);      // both's scales
-    static constexpr int kBytes = kValues + kCodes + kScales;
+    static constexpr int kValueRow = 2 * D + 16;              // bytes of a position's values in LDS
+    static constexpr int kCodes = 32 * kValueRow;             // V, then K from here,
+    static constexpr int kScales = kCodes + 32 * D;           // then K's scales,
+    static constexpr int kOdd = kScales + 32 * (D / 32);      // then whether values are no numbers, a byte a wave
+    static constexpr int kBytes = kOdd + 16;
     // where piece `piece` of position `key`'s codes is
     __device__ static int code_at(int key, int piece) {
-        return key * D + (piece ^ (key / (256 / D) % kLanes)) * 16;
+        return kCodes + key * D + (piece ^ (key / (256 / D) % kLanes)) * 16;
     }
 };
 
-// 32 positions' keys and values as loaded: lane l has piece l % kLanes of
-// position kKeys i + l / kLanes; the scales of position l % 32, lanes 0 .. 31
-// of K, the others of V
-template <int D>
-struct Raw {
-    u32x4_t k[Tile<D>::kLoads], v[Tile<D>::kLoads];
-    uint64_t scales;  // D / 32 bytes
-    bool ok[2];    // the page of the first 16 positions and of the others is one of the cache's
+// A wave's part of a tile as loaded: lane l has piece l % kLanes of position
+// kKeys i + l / kLanes, that value's scale, and all scales of that key
+template <int D, int N>
+struct Part {
+    u32x4_t k[N], v[N];
+    uint32_t vs[N];
+    typename Tile<D>::scales_t ks[N];
 };
 
-// page numbers of positions p0 .. p0+15 and p0+16 .. p0+31 (-1: none)
+// Page numbers of a tile's two halves, as the table has them.  Loads that are
+// on their way are not chosen between nor copied (either waits for them): past
+// the last position its page is asked for again.
 __device__ inline void page_numbers(const AttnArgs& p, const int32_t* table, int p0, int len, int (&page)[2]) {
 #pragma unroll
-    for (int t = 0; t < 2; t++) page[t] = p0 + 16 * t < len ? table[(p0 + 16 * t) >> p.page_shift] : -1;
+    for (int t = 0; t < 2; t++) page[t] = table[max(min(p0 + 16 * t, len - 1), 0) >> p.page_shift];
 }
 
-template <int D>
-__device__ inline void load_raw(const AttnArgs& p, int h, int p0, const int (&page)[2], Raw<D>& r) {
-    using T = Tile<D>;
-    const moe_kv_cache& q = p.a.cache;
-    const uint32_t lane = threadIdx.x % kWave;
-    int64_t at[2];
-    int row[2];
+// Whether the two halves are there, in pages of the cache, and the numbers to
+// load from (page 0 for a half that is not)
+struct Pages {
+    int number[2];
+    bool ok[2];
+};
+__device__ inline Pages pages_of(const AttnArgs& p, const int (&page)[2], int p0, int len) {
+    Pages g;
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-        const int number = uniform(page[t]);
-        r.ok[t] = (uint32_t)number < (uint32_t)q.num_pages;
-        at[t] = r.ok[t] ? number : 0;
-        row[t] = h * q.page_size + ((p0 + 16 * t) & (q.page_size - 1));
+        const int n = uniform(page[t]);
+        g.ok[t] = p0 + 16 * t < len && (uint32_t)n < (uint32_t)p.a.cache.num_pages;
+        g.number[t] = g.ok[t] ? n : 0;
     }
+    return g;
+}
+
+template <int D, int N>
+__device__ inline void load_part(const AttnArgs& p, int h, int p0, int wr, const Pages& g, Part<D, N>& r) {
+    using T = Tile<D>;
+    const moe_kv_cache& q = p.a.cache;
+    const uint32_t lane = threadIdx.x % kWave, key = lane / T::kLanes, piece = lane % T::kLanes;
 #pragma unroll
-    for (int i = 0; i < T::kLoads; i++) {
-        const int t = i * T::kKeys / 16;
-        const int64_t code = at[t] * q.codes_page_stride + (int64_t)(row[t] + i * T::kKeys % 16) * D;
+    for (int i = 0; i < N; i++) {
+        const int first = (wr * N + i) * T::kKeys, t = first / 16;
+        const int64_t page = t ? g.number[1] : g.number[0];
+        const int64_t row = h * q.page_size + ((p0 + first) & (q.page_size - 1));
+        const int64_t code = page * q.codes_page_stride + row * D, scale = page * q.scales_page_stride + row * (D / 32);
         r.k[i] = *reinterpret_cast<const u32x4_t*>(q.k_codes + code + lane * 16);
         r.v[i] = *reinterpret_cast<const u32x4_t*>(q.v_codes + code + lane * 16);
+        r.vs[i] = (q.v_scales + scale)[key * (D / 32) + piece / 2];
+        r.ks[i] = reinterpret_cast<const typename T::scales_t*>(q.k_scales + scale)[key];
     }
-    const int t = lane / 16 % 2;
-    const uint8_t* s = (lane < 32 ? q.k_scales : q.v_scales) +
-                       ((t ? at[1] : at[0]) * q.scales_page_stride + (int64_t)(t ? row[1] : row[0]) * (D / 32)) +
-                       lane % 16 * (D / 32);
-    if constexpr (D == 64) r.scales = *reinterpret_cast<const uint16_t*>(s);
-    else if constexpr (D == 128) r.scales = *reinterpret_cast<const uint32_t*>(s);
-    else r.scales = *reinterpret_cast<const uint64_t*>(s);
 }
 
 __device__ inline f32x4_t mfma(const bf16x8_t& a, const bf16x8_t& b, const f32x4_t& c) {
@@ -213,6 +233,13 @@ __device__ inline f32x4_t mfma(const bf16x8_t& a, const bf16x8_t& b, const f32x4
 __device__ inline void wave_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+}
+
+// A barrier that orders LDS alone: loads from memory stay on their way
+__device__ inline void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Which of positions p0 .. p0+31 a drafted token sees (bit k: p0 + k)
@@ -260,65 +287,82 @@ struct Wave {
     float pass[R];      // the score past which the reference is moved
 };
 
-// One step: 32 positions from p0.  `ahead` issues the next step's loads.
-template <int D, int R, typename Ahead>
+// A value that is no number makes one of what sees it, and of nothing else.
+// 2^127 in its place is multiplied with 2^127 where it is seen, and with the
+// negative: infinity, then infinity less infinity.  The rest is returned, with
+// zeros in those places.
+template <int D, int R>
+__device__ inline bf16x8_t take_specials(const bf16x8_t& vt, const uint32_t (&seen)[R], int d, Wave<D, R>& w) {
+    u32x4_t v = __builtin_bit_cast(u32x4_t, vt), n, m;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        n[i] = specials(v[i]);
+        m[i] = n[i] | (n[i] << 1 & 0x80008000u);
+        v[i] &= ~((n[i] & 0x4000u ? 0xffffu : 0u) | (n[i] & 0x40000000u ? 0xffff0000u : 0u));
+    }
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        auto pair = [&](int k) {  // of positions k, k + 1
+            return 0x7f00u * (seen[r] >> k & 1u) | 0x7f000000u * (seen[r] >> (k + 1) & 1u);
+        };
+        const u32x4_t sees = {pair(0), pair(2), pair(16), pair(18)};
+        w.o[r][d] = mfma(__builtin_bit_cast(bf16x8_t, n), __builtin_bit_cast(bf16x8_t, sees), w.o[r][d]);
+        w.o[r][d] = mfma(__builtin_bit_cast(bf16x8_t, m), __builtin_bit_cast(bf16x8_t, sees), w.o[r][d]);
+    }
+    return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// A wave's part of the tile at p0, into LDS.  `special`: some of the tile's
+// positions are drafted ones or none at all; else all rows see all of them.
+template <int D, int N>
+__device__ inline void store_part(const Seq& s, int p0, int wr, bool special, const Pages& g, Part<D, N>& r,
+                                  uint8_t* lds) {
+    using T = Tile<D>;
+    const int lane = threadIdx.x % kWave, key = lane / T::kLanes, piece = lane % T::kLanes;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int at = (wr * N + i) * T::kKeys + key;
+        *reinterpret_cast<u32x4_t*>(lds + T::code_at(at, piece)) = r.k[i];
+        if (piece == 0) reinterpret_cast<typename T::scales_t*>(lds + T::kScales)[at] = r.ks[i];
+        if (special) {
+            if (!(p0 + at < s.len && ((wr * N + i) * T::kKeys >= 16 ? g.ok[1] : g.ok[0]))) {  // nothing is there
+                r.v[i] = u32x4_t{0, 0, 0, 0};
+                r.vs[i] = 0;
+            }
+            odd |= has_specials(r.v[i], r.vs[i]);
+        }
+        const float f = e8m0_as_scale(r.vs[i]);
+        bf16x8_t* v = reinterpret_cast<bf16x8_t*>(lds + at * T::kValueRow + piece * 32);
+        v[0] = decode8_e4m3(r.v[i].x, r.v[i].y, f);
+        v[1] = decode8_e4m3(r.v[i].z, r.v[i].w, f);
+    }
+    if (special) {
+        odd = __any(odd);
+        if (lane == 0) lds[T::kOdd + wr] = odd;
+    }
+}
+
+// One step: the 32 positions from p0, whose tile is in LDS, for a wave's rows
+template <int D, int R, int WR>
 __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R], const bf16x8_t (&q)[R][D / 32],
-                            int p0, Raw<D>& raw, uint8_t* lds, Wave<D, R>& w, Ahead&& ahead) {
+                            int p0, bool special, bool ok0, bool ok1, const uint8_t* lds, Wave<D, R>& w) {
     using T = Tile<D>;
     const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
-    const int key = lane / T::kLanes, piece = lane % T::kLanes;  // of a load
-    uint8_t *codes = lds + T::kValues, *scales = codes + T::kCodes;
-    // K and the scales as they are
-    if constexpr (D == 64) *reinterpret_cast<uint16_t*>(scales + lane * 2) = (uint16_t)raw.scales;
-    else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(scales + lane * 4) = (uint32_t)raw.scales;
-    else *reinterpret_cast<uint64_t*>(scales + lane * 8) = raw.scales;
-#pragma unroll
-    for (int i = 0; i < T::kLoads; i++)
-        *reinterpret_cast<u32x4_t*>(codes + T::code_at(T::kKeys * i + key, piece)) = raw.k[i];
-    wave_order();
-    // V in bf16
-    uint32_t vs[T::kLoads];
-#pragma unroll
-    for (int i = 0; i < T::kLoads; i++) vs[i] = scales[(32 + T::kKeys * i + key) * (D / 32) + piece / 2];
-    const bool ok0 = raw.ok[0], ok1 = raw.ok[1];
-    // whether some of them are drafted ones or none at all; else all rows see all
-    const bool special = p0 + 32 > s.L || !ok0 || !ok1;
-    bool odd = false;  // a drafted token's value is no number
-    if (special) {
-#pragma unroll
-        for (int i = 0; i < T::kLoads; i++) {
-            if (!(p0 + T::kKeys * i + key < s.len && (i * T::kKeys / 16 ? ok1 : ok0))) {  // nothing is there
-                raw.v[i] = u32x4_t{0, 0, 0, 0};
-                vs[i] = 0;
-            }
-            odd |= has_specials(raw.v[i], vs[i]);
-        }
-        odd = __any(odd);
-    }
-    uint8_t* mine = lds + key * T::kValueRow + piece * 32;
-#pragma unroll
-    for (int i = 0; i < T::kLoads; i++) {
-        const float f = e8m0_as_scale(vs[i]);
-        bf16x8_t* at = reinterpret_cast<bf16x8_t*>(mine + T::kKeys * i * T::kValueRow);
-        at[0] = decode8_e4m3(raw.v[i].x, raw.v[i].y, f);
-        at[1] = decode8_e4m3(raw.v[i].z, raw.v[i].w, f);
-    }
-    wave_order();
-    ahead();
-
     f32x4_t st[2][R];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
 #pragma unroll
         for (int r = 0; r < R; r++) st[t][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         // lane (c, g): quarter g of position 16 t + c
+        const uint8_t* scales = lds + T::kScales + (16 * t + c) * (D / 32);
         uint32_t ks = 0;
-        if constexpr (D == 64) ks = scales[(16 * t + c) * 2 + g / 2];
-        else if constexpr (D == 128) ks = scales[(16 * t + c) * 4 + g];
-        else ks = *reinterpret_cast<const uint16_t*>(scales + (16 * t + c) * 8 + 2 * g);
+        if constexpr (D == 64) ks = scales[g / 2];
+        else if constexpr (D == 128) ks = scales[g];
+        else ks = *reinterpret_cast<const uint16_t*>(scales + 2 * g);
 #pragma unroll
         for (int j = 0; j < D / 64; j++) {
-            const uint4 x = *reinterpret_cast<const uint4*>(codes + T::code_at(16 * t + c, g * (D / 64) + j));
+            const u32x4_t x = *reinterpret_cast<const u32x4_t*>(lds + T::code_at(16 * t + c, g * (D / 64) + j));
             const float f = e8m0_as_scale(D == 256 ? (j < 2 ? ks & 0xffu : ks >> 8) : ks);
             const bf16x8_t k0 = decode8_e4m3(x.x, x.y, f), k1 = decode8_e4m3(x.z, x.w, f);
 #pragma unroll
@@ -340,8 +384,9 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
     bf16x8_t vt[kAhead];
 #pragma unroll
     for (int d = 0; d < kAhead; d++) vt[d] = value(d);
-    __builtin_amdgcn_sched_barrier(0);
+
     uint32_t seen[R];
+    bool odd = false;  // a value is no number
     if (special) {
 #pragma unroll
         for (int r = 0; r < R; r++) {
@@ -354,6 +399,10 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
                     st[t][r][i] = __uint_as_float((__float_as_uint(st[t][r][i]) & keep) | (0xff800000u & ~keep));
                 }
         }
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < WR; i++) any |= lds[T::kOdd + i];
+        odd = uniform(any) != 0;
     }
     // the reference score, where one has passed it
     float top[R];
@@ -393,65 +442,34 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
     const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, one16);
 #pragma unroll
     for (int r = 0; r < R; r++) w.sum[r] = mfma(ones, pt[r], w.sum[r]);
-
-    if (odd) {
-        // A value that is no number makes one of what sees it, and of
-        // nothing else.  2^127 in its place is multiplied with 2^127 where
-        // it is seen, and with the negative: infinity, then infinity less
-        // infinity.  For the product below it is then zero.
-#pragma unroll
-        for (int r = 0; r < R; r++) {
-            auto pair = [&](int k) {  // of positions k, k + 1
-                return 0x7f00u * (seen[r] >> k & 1u) | 0x7f000000u * (seen[r] >> (k + 1) & 1u);
-            };
-            const uint4 sees = make_uint4(pair(0), pair(2), pair(16), pair(18));
-#pragma unroll
-            for (int d = 0; d < D / 16; d++) {
-                const uint4 v = __builtin_bit_cast(uint4, value(d));
-                const uint4 n = make_uint4(specials(v.x), specials(v.y), specials(v.z), specials(v.w));
-                const uint4 m = make_uint4(n.x | (n.x << 1 & 0x80008000u), n.y | (n.y << 1 & 0x80008000u),
-                                           n.z | (n.z << 1 & 0x80008000u), n.w | (n.w << 1 & 0x80008000u));
-                w.o[r][d] = mfma(__builtin_bit_cast(bf16x8_t, n), __builtin_bit_cast(bf16x8_t, sees), w.o[r][d]);
-                w.o[r][d] = mfma(__builtin_bit_cast(bf16x8_t, m), __builtin_bit_cast(bf16x8_t, sees), w.o[r][d]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-        wave_order();
-#pragma unroll 1
-        for (int i = 0; i < 2 * T::kLoads; i++) {
-            uint4* at = reinterpret_cast<uint4*>(mine + i / 2 * T::kKeys * T::kValueRow + i % 2 * 16);
-            const uint4 v = *at;
-            auto clean = [](uint32_t x) { const uint32_t n = specials(x);
-                return x & ~((n & 0x4000u ? 0xffffu : 0u) | (n & 0x40000000u ? 0xffff0000u : 0u)); };
-            *at = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
-        }
-        wave_order();
-#pragma unroll
-        for (int d = 0; d < kAhead; d++) vt[d] = value(d);
-    }
 #pragma unroll
     for (int d = 0; d < D / 16; d++) {
+        if (odd) vt[d % kAhead] = take_specials<D, R>(vt[d % kAhead], seen, d, w);
 #pragma unroll
         for (int r = 0; r < R; r++) w.o[r][d] = mfma(vt[d % kAhead], pt[r], w.o[r][d]);
         if (d + kAhead < D / 16) vt[d % kAhead] = value(d + kAhead);
     }
-    wave_order();
 }
 
 // the statistic of rows without a position is -infinity: their weight is 0
 __device__ inline float reference(float m) { return m == minus_inf() ? 0.f : m; }
 
 // A workgroup's shape: WR groups of 16 R rows times WK runs of positions, a
-// wave each.
+// wave each.  The WR waves of a run share its tiles, which are then in LDS twice:
+// the next one's parts are stored while this one is worked on.
 template <int D_, int R_, int WR_, int WK_>
 struct Shape {
     static constexpr int D = D_, R = R_, WR = WR_, WK = WK_;
     static constexpr int kRows = 16 * R * WR, kWaves = WR * WK, kThreads = kWave * kWaves;
-    // a wave's 32 positions; at the end the waves' results, 16 rows of each
-    static constexpr int kTile = Tile<D>::kBytes, kResult = 16 * (D + 4) * 4;
-    static constexpr int kLds = kWaves * (kTile > kResult ? kTile : kResult);
-    // waves per SIMD that the registers leave room for
-    static constexpr int kPerSimd = D == 256 ? 1 : D * R <= 128 ? 3 : 2;
+    static constexpr int kParts = Tile<D>::kLoads / WR;
+    static_assert(kParts * WR == Tile<D>::kLoads, "a tile is dealt evenly");
+    static constexpr int kBuffers = WR == 1 ? 1 : 2, kTiles = kBuffers * WK * Tile<D>::kBytes;
+    static constexpr int kResult = kWaves * 16 * (D + 4) * 4;  // at the end the waves' results, 16 rows of each
+    static constexpr int kQuery = 16 * D * 2;                  // at the start 16 queries of each
+    static constexpr int kLds = kTiles > kResult ? kTiles : kResult;
+    static_assert(kWaves * kQuery <= kLds, "queries fit");
+    // waves per SIMD that the registers and LDS leave room for
+    static constexpr int kPerSimd = D == 256 ? 1 : D == 64 && R == 1 ? 3 : 2;
 };
 
 template <typename S>
@@ -464,39 +482,76 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
     // Workgroups are dealt round the 8 XCDs; each XCD takes a run of the line, so
     // that the row tiles of a head, which read the same positions, share its L2
     const int group = (int)blockIdx.x % 8 * (p.groups / 8) + (int)blockIdx.x / 8;
-    const Line line = line_of<ROWS>(p);
+    Line line = line_of<ROWS>(p);
     int u = uniform(group * line.per);
     const int end = uniform(min(u + line.per, line.total));
     if (u >= end) return;
     int base = 0;
-    int b = uniform(sequence_at<ROWS>(p, u, false, &base));
-    base = uniform(base);
+    Seq s;
+    int b = uniform(sequence_at<ROWS>(p, u, false, &line, &s, &base));
     while (u < end) {
-        Seq s = read_seq(p, b);
-        s.first = uniform(s.first), s.n = uniform(s.n), s.L = uniform(s.L), s.len = uniform(s.len);
-        const int tiles = tiles_of<ROWS>(p, s), units = units_of(s), all = s.n ? tiles * units * p.a.cache.kv_heads : 0;
+        const int tiles = tiles_of<ROWS>(p, s), units = units_of(s), all = weight_of<ROWS>(p, s);
         if (u - base >= all) {  // on to the next sequence (there is one: u < total)
             base += all;
             b++;
+            s = read_seq(p, b);
+            s.first = uniform(s.first), s.n = uniform(s.n), s.L = uniform(s.L), s.len = uniform(s.len);
             continue;
         }
         const int item = (u - base) / units, u0 = (u - base) % units, u1 = min(units, u0 + end - u);
         const int h = item / tiles, row0 = item % tiles * ROWS, rows = s.n * p.G;
 
+        // positions that some row of the workgroup, and of the wave, may see
+        const int from = u0 * kAttnUnit;
+        int stop = min(s.len, u1 * kAttnUnit), mine = stop;
+        if (!p.a.mask) {
+            stop = min(stop, s.L + (min(row0 + ROWS, rows) - 1) / p.G + 1);
+            mine = min(stop, s.L + (min(row0 + 16 * R * (wr + 1), rows) - 1) / p.G + 1);
+        }
+        if (row0 + 16 * R * wr >= rows) mine = 0;
+        const int32_t* table = p.a.block_table + (int64_t)b * p.a.block_table_stride;
+        const int steps = stop > from ? (stop - from + 32 * WK - 1) / (32 * WK) : 0;
+        int p0 = from + 32 * wk;
+        int page[2];
+        page_numbers(p, table, p0, s.len, page);
+
         int node[R];
         bf16x8_t q[R][D / 32];
         Wave<D, R> w;
+        // the queries, whole lines at a time and through LDS (past the last row that row again)
+        constexpr int kRowLanes = D / 8, kRowsAtOnce = kWave / kRowLanes;  // lanes of 16 bytes a row
+        u32x4_t rows_in[R][16 / kRowsAtOnce];
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            const int row = row0 + 16 * (R * wr + r) + c, live = row < rows;
-            node[r] = (live ? row : rows - 1) / p.G;
-            const uint16_t* src = (const uint16_t*)p.a.q + (int64_t)(s.first + node[r]) * p.a.q_stride +
-                                  (h * p.G + (live ? row % p.G : 0)) * D + g * (D / 4);
+            node[r] = (min(row0 + 16 * (R * wr + r) + c, rows - 1)) / p.G;
 #pragma unroll
-            for (int j = 0; j < D / 32; j++) {
-                const uint4 x = live ? reinterpret_cast<const uint4*>(src)[j] : make_uint4(0, 0, 0, 0);
-                q[r][j] = __builtin_bit_cast(bf16x8_t, x);
+            for (int i = 0; i < 16 / kRowsAtOnce; i++) {
+                const int at = min(row0 + 16 * (R * wr + r) + kRowsAtOnce * i + lane / kRowLanes, rows - 1);
+                const int head = at % p.G;
+                const uint16_t* src = (const uint16_t*)p.a.q + (int64_t)(s.first + at / p.G) * p.a.q_stride +
+                                      (h * p.G + head) * D + lane % kRowLanes * 8;
+                rows_in[r][i] = *reinterpret_cast<const u32x4_t*>(src);
             }
+        }
+        Part<D, S::kParts> part;
+        Pages pages = pages_of(p, page, p0, s.len);
+        load_part(p, h, p0, wr, pages, part);
+        page_numbers(p, table, p0 + 32 * WK, s.len, page);
+        uint8_t* qbuf = buf + wave * S::kQuery;
+        auto query_at = [](int row, int piece) {  // 16-byte pieces, the 16 rows' in different banks
+            return row * D * 2 + (piece ^ (D == 64 ? row / 2 : row)) * 16;
+        };
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+#pragma unroll
+            for (int i = 0; i < 16 / kRowsAtOnce; i++)
+                *reinterpret_cast<u32x4_t*>(qbuf + query_at(kRowsAtOnce * i + lane / kRowLanes, lane % kRowLanes)) =
+                    rows_in[r][i];
+            wave_order();
+#pragma unroll
+            for (int j = 0; j < D / 32; j++)
+                q[r][j] = *reinterpret_cast<const bf16x8_t*>(qbuf + query_at(c, g * (D / 32) + j));
+            wave_order();
 #pragma unroll
             for (int d = 0; d < D / 16; d++) w.o[r][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
             w.sum[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -504,30 +559,45 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             w.mc[r] = 0.f;
             w.pass[r] = minus_inf();
         }
-        // positions that some row of the wave may see
-        int stop = s.len;
-        if (!p.a.mask) stop = min(stop, s.L + (min(row0 + 16 * R * (wr + 1), rows) - 1) / p.G + 1);
-        stop = row0 + 16 * R * wr < rows ? min(stop, u1 * kAttnUnit) : 0;
-        const int32_t* table = p.a.block_table + (int64_t)b * p.a.block_table_stride;
-        int p0 = u0 * kAttnUnit + 32 * wk;
-        if (p0 < stop) {
-            Raw<D> raw;
-            int page[2];
-            page_numbers(p, table, p0, s.len, page);
-            load_raw<D>(p, h, p0, page, raw);
-            page_numbers(p, table, p0 + 32 * WK, s.len, page);
-            uint8_t* lds = buf + wave * S::kTile;
-            for (; p0 < stop; p0 += 32 * WK) {
-                auto ahead = [&] {
-                    const int next = p0 + 32 * WK;
-                    if (next < stop) {
-                        load_raw<D>(p, h, next, page, raw);
-                        page_numbers(p, table, next + 32 * WK, s.len, page);
-                    }
-                };
-                step<D, R>(p, s, node, q, p0, raw, lds, w, ahead);
+        lds_barrier();
+
+        uint8_t* tile = buf + S::kBuffers * wk * Tile<D>::kBytes;
+        auto is_special = [&](int at, const Pages& g) { return at + 32 > s.L || !g.ok[0] || !g.ok[1]; };
+        // the part that is to be loaded next is `ahead` tiles on
+        auto load_next = [&](int ahead) {
+            const int at = p0 + ahead * 32 * WK;
+            pages = pages_of(p, page, at, s.len);
+            load_part(p, h, at, wr, pages, part);
+            page_numbers(p, table, at + 32 * WK, s.len, page);
+        };
+        if constexpr (WR == 1) {  // a tile is its wave's own
+            for (int i = 0; i < steps && p0 < mine; i++, p0 += 32 * WK) {
+                const Pages now = pages;
+                const bool special = is_special(p0, now);
+                store_part(s, p0, wr, special, now, part, tile);
+                wave_order();
+                load_next(1);
+                step<D, R, WR>(p, s, node, q, p0, special, now.ok[0], now.ok[1], tile, w);
+                wave_order();
+            }
+        } else if (steps > 0) {
+            store_part(s, p0, wr, is_special(p0, pages), pages, part, tile);
+            Pages now = pages;
+            load_next(1);
+            lds_barrier();
+            for (int i = 0; i < steps; i++, p0 += 32 * WK) {
+                const Pages then = pages;
+                const int next = p0 + 32 * WK;
+                store_part(s, next, wr, is_special(next, pages), pages, part, tile + (~i & 1) * Tile<D>::kBytes);
+                load_next(2);
+                if (p0 < mine)
+                    step<D, R, WR>(p, s, node, q, p0, is_special(p0, now), now.ok[0], now.ok[1],
+                                   tile + (i & 1) * Tile<D>::kBytes, w);
+                now = then;
+                lds_barrier();
             }
         }
+        lds_barrier();
 
         // the results of the waves of a row group joined, 16 rows of each group at a time
         if (g == 0)
@@ -542,7 +612,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             return m;
         };
         const bool whole = u0 == 0 && u1 == units;
-        float* part = (float*)p.a.workspace + (2 * (int64_t)group + (u0 ? 0 : 1)) * p.part_floats;
+        float* left = (float*)p.a.workspace + (2 * (int64_t)group + (u0 ? 0 : 1)) * p.part_floats;
         float* joined = reinterpret_cast<float*>(buf);
         constexpr int kPiece = D * 16 * WR / S::kThreads, kPieces = D / kPiece;  // of a row: elements of a thread, threads
 #pragma unroll
@@ -565,12 +635,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
                 for (int d = 0; d < kPiece; d++) v[d] += joined[((og * WK + i) * 16 + orow) * (D + 4) + d0 + d];
             }
             if (!whole) {
-                float* dst = part + at * D + d0;
+                float* dst = left + at * D + d0;
 #pragma unroll
                 for (int d = 0; d < kPiece; d++) dst[d] = v[d];
                 if (d0 == 0) {
-                    part[ROWS * D + 2 * at] = top_of(at);
-                    part[ROWS * D + 2 * at + 1] = sum;
+                    left[ROWS * D + 2 * at] = top_of(at);
+                    left[ROWS * D + 2 * at + 1] = sum;
                 }
             } else if (row0 + at < rows) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -597,12 +667,11 @@ __global__ void __launch_bounds__(kJoinWaves * kWave) tree_attention_join_kernel
     const int idx = uniform((int)blockIdx.x * kJoinWaves + (int)threadIdx.x / kWave);
     if (idx >= p.T * p.a.num_heads) return;
     const int token = idx / p.a.num_heads, head = idx % p.a.num_heads;
-    const Line line = line_of<ROWS>(p);
+    Line line = line_of<ROWS>(p);
     if (line.total == 0) return;
     int base = 0;
-    const int b = uniform(sequence_at<ROWS>(p, token, true, &base));
-    if (b < 0) return;
-    const Seq s = read_seq(p, b);
+    Seq s;
+    if (sequence_at<ROWS>(p, token, true, &line, &s, &base) < 0) return;
     const int units = units_of(s), row = (token - s.first) * p.G + head % p.G, at = row % ROWS;
     const int u0 = base + (head / p.G * tiles_of<ROWS>(p, s) + row / ROWS) * units;
     const int first = u0 / line.per, parts = (u0 + units - 1) / line.per - first + 1;
@@ -649,13 +718,18 @@ hipError_t launch_shape(const AttnArgs& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int D, int W>  // W: waves of the larger shapes
+template <int D>
 hipError_t launch_rows(const AttnArgs& p, int rows, hipStream_t stream) {
-    switch (rows) {
-        case 16: return launch_shape<D, 1, 1, 4>(p, stream);
-        case 32: return launch_shape<D, 2, 1, 4>(p, stream);
-        case 64: return launch_shape<D, 2, 2, W / 2>(p, stream);
-        default: return launch_shape<D, 2, 4, W / 4>(p, stream);
+    if (rows == 16) return launch_shape<D, 1, 1, 4>(p, stream);
+    if constexpr (D == 256) {
+        return rows == 32   ? launch_shape<D, 1, 2, 2>(p, stream)
+               : rows == 64 ? launch_shape<D, 1, 4, 1>(p, stream)
+                            : launch_shape<D, 2, 4, 1>(p, stream);
+    } else {
+        if (rows == 32) return launch_shape<D, 2, 1, 4>(p, stream);
+        if constexpr (D == 128)
+            if (rows == 128) return launch_shape<D, 2, 4, 2>(p, stream);
+        return launch_shape<D, 2, 2, 4>(p, stream);
     }
 }
 
@@ -675,9 +749,9 @@ hipError_t launch_tree_attention(const moe_tree_attention_args& a, hipStream_t s
     p.c = a.scale * 1.44269504088896340736f;
     p.part_floats = plan.part_floats;
     switch (a.cache.head_dim) {
-        case 64: return launch_rows<64, 8>(p, plan.rows, stream);
-        case 128: return launch_rows<128, 8>(p, plan.rows, stream);
-        default: return launch_rows<256, 4>(p, plan.rows, stream);
+        case 64: return launch_rows<64>(p, plan.rows, stream);
+        case 128: return launch_rows<128>(p, plan.rows, stream);
+        default: return launch_rows<256>(p, plan.rows, stream);
     }
 }
 
