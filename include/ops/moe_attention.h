@@ -57,7 +57,7 @@ typedef struct moe_kv_cache {
     uint8_t* k_scales;          /* [num_pages, kv_heads, page_size, head_dim / 32] E8M0 */
     uint8_t* v_codes;
     uint8_t* v_scales;
-    int64_t codes_page_stride;  /* bytes from page to page, at least one page's; 0: one page's */
+    int64_t codes_page_stride;  /* bytes from page to page, at least one page's, up to 2^31; 0: one page's */
     int64_t scales_page_stride;
     int64_t num_pages;          /* 1 .. 2^31 - 1 */
     int32_t page_size;          /* 16, 32, 64, .. 1024 */

@@ -9,7 +9,7 @@ namespace {
 
 using moe::hip_fail;
 
-constexpr int64_t kMaxStride = 1ll << 40, kMaxTokens = 1ll << 20, kMaxSeqs = 1ll << 16;
+constexpr int64_t kMaxStride = 1ll << 40, kMaxPageStride = 1ll << 31, kMaxTokens = 1ll << 20, kMaxSeqs = 1ll << 16;
 constexpr int64_t kMaxPositions = 1ll << 30, kMaxUnits = 1ll << 30;
 constexpr int kMaxHeads = 1024, kMaxMaskWords = 64;
 
@@ -29,8 +29,8 @@ int check_cache_sizes(moe_kv_cache* c) {
     if (c->kv_heads < 1 || c->kv_heads > kMaxHeads) return MOE_E_SHAPE;
     if (c->head_dim < 32 || c->head_dim > 512 || c->head_dim % 32) return MOE_E_SHAPE;
     const int64_t page = (int64_t)c->kv_heads * c->page_size * c->head_dim;
-    return fill_stride(&c->codes_page_stride, page) || fill_stride(&c->scales_page_stride, page / 32) ? MOE_E_SHAPE
-                                                                                                       : MOE_OK;
+    if (fill_stride(&c->codes_page_stride, page) || fill_stride(&c->scales_page_stride, page / 32)) return MOE_E_SHAPE;
+    return c->codes_page_stride > kMaxPageStride || c->scales_page_stride > kMaxPageStride ? MOE_E_SHAPE : MOE_OK;
 }
 
 int check_cache_memory(const moe_kv_cache& c) {

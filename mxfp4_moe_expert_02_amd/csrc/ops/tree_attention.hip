@@ -164,7 +164,8 @@ struct Tile {
     static constexpr int kValueRow = 2 * D + 16;              // bytes of a position's values in LDS
     static constexpr int kCodes = 32 * kValueRow;             // V, then K from here,
     static constexpr int kScales = kCodes + 32 * D;           // then K's scales,
-    static constexpr int kOdd = kScales + 32 * (D / 32);      // then whether values are no numbers, a byte a wave
+    static constexpr int kBits = kScales + 32 * (D / 32);     // then for drafted positions a bit for each value that is
+    static constexpr int kOdd = kBits + 32 * (D / 8);         // no number, then whether there are any, a byte a wave
     static constexpr int kBytes = kOdd + 16;
     // where piece `piece` of position `key`'s codes is
     __device__ static int code_at(int key, int piece) {
@@ -181,46 +182,66 @@ struct Part {
     typename Tile<D>::scales_t ks[N];
 };
 
-// Page numbers of a tile's two halves, as the table has them.  Loads that are
-// on their way are not chosen between nor copied (either waits for them): past
-// the last position its page is asked for again.
-__device__ inline void page_numbers(const AttnArgs& p, const int32_t* table, int p0, int len, int (&page)[2]) {
-#pragma unroll
-    for (int t = 0; t < 2; t++) page[t] = table[max(min(p0 + 16 * t, len - 1), 0) >> p.page_shift];
+// The page numbers of a wave's tiles, 32 tiles at a time: lane l has that of half
+// l % 2 of tile l / 2, as the table has it (past the last position its page is
+// asked for again).  Read one by one a step before they are needed they would
+// each be waited for: a value that is the same in all lanes goes to a scalar
+// register as soon as it is there.
+struct PageRun {
+    int now, next;
+};
+__device__ inline int page_numbers(const AttnArgs& p, const int32_t* table, int p0, int stride, int len) {
+    const int lane = threadIdx.x % kWave;
+    const int64_t at = p0 + (int64_t)(lane / 2) * stride + 16 * (lane % 2);
+    return table[max((int)(at < len ? at : len - 1), 0) >> p.page_shift];
 }
 
-// Whether the two halves are there, in pages of the cache, and the numbers to
-// load from (page 0 for a half that is not)
-struct Pages {
-    int number[2];
+// A tile's two halves: whether they are there, in pages of the cache, and
+// their numbers (page 0 for one that is not)
+struct Halves {
+    uint32_t number[2];
     bool ok[2];
 };
-__device__ inline Pages pages_of(const AttnArgs& p, const int (&page)[2], int p0, int len) {
-    Pages g;
+__device__ inline Halves halves_of(const AttnArgs& p, int pages, int tile, int p0, int len) {
+    Halves h;
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-        const int n = uniform(page[t]);
-        g.ok[t] = p0 + 16 * t < len && (uint32_t)n < (uint32_t)p.a.cache.num_pages;
-        g.number[t] = g.ok[t] ? n : 0;
+        const uint32_t n = (uint32_t)__builtin_amdgcn_readlane(pages, 2 * (tile % 32) + t);
+        h.ok[t] = p0 + 16 * t < len && n < (uint32_t)p.a.cache.num_pages;
+        h.number[t] = h.ok[t] ? n : 0u;
     }
-    return g;
+    return h;
+}
+
+// What a lane's addresses start from: page 0 of a head
+struct Bases {
+    const uint8_t *k, *v, *ks, *vs;
+};
+template <int D>
+__device__ inline Bases bases_of(const moe_kv_cache& q, int h) {
+    using T = Tile<D>;
+    const uint32_t lane = threadIdx.x % kWave, key = lane / T::kLanes, piece = lane % T::kLanes;
+    const int64_t row = (int64_t)h * q.page_size;
+    return Bases{q.k_codes + row * D + lane * 16, q.v_codes + row * D + lane * 16,
+                 q.k_scales + row * (D / 32) + key * (D / 32), q.v_scales + row * (D / 32) + key * (D / 32) + piece / 2};
 }
 
 template <int D, int N>
-__device__ inline void load_part(const AttnArgs& p, int h, int p0, int wr, const Pages& g, Part<D, N>& r) {
+__device__ inline void load_part(const AttnArgs& p, const Bases& base, int p0, int wr, const Halves& h,
+                                 Part<D, N>& r) {
     using T = Tile<D>;
     const moe_kv_cache& q = p.a.cache;
-    const uint32_t lane = threadIdx.x % kWave, key = lane / T::kLanes, piece = lane % T::kLanes;
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        const int first = (wr * N + i) * T::kKeys, t = first / 16;
-        const int64_t page = t ? g.number[1] : g.number[0];
-        const int64_t row = h * q.page_size + ((p0 + first) & (q.page_size - 1));
-        const int64_t code = page * q.codes_page_stride + row * D, scale = page * q.scales_page_stride + row * (D / 32);
-        r.k[i] = *reinterpret_cast<const u32x4_t*>(q.k_codes + code + lane * 16);
-        r.v[i] = *reinterpret_cast<const u32x4_t*>(q.v_codes + code + lane * 16);
-        r.vs[i] = (q.v_scales + scale)[key * (D / 32) + piece / 2];
-        r.ks[i] = reinterpret_cast<const typename T::scales_t*>(q.k_scales + scale)[key];
+        const int first = (wr * N + i) * T::kKeys;
+        const uint64_t n = first >= 16 ? h.number[1] : h.number[0];
+        const uint32_t row = (p0 + first) & (q.page_size - 1);
+        const uint64_t code = n * (uint32_t)q.codes_page_stride + row * D;
+        const uint64_t scale = n * (uint32_t)q.scales_page_stride + row * (D / 32);
+        r.k[i] = *reinterpret_cast<const u32x4_t*>(base.k + code);
+        r.v[i] = *reinterpret_cast<const u32x4_t*>(base.v + code);
+        r.ks[i] = *reinterpret_cast<const typename T::scales_t*>(base.ks + scale);
+        r.vs[i] = base.vs[scale];
     }
 }
 
@@ -266,19 +287,6 @@ __device__ inline uint32_t seen_bits(const AttnArgs& p, const Seq& s, int node, 
     return seen & (ok0 ? ~0u : 0xffff0000u) & (ok1 ? ~0u : 0xffffu);
 }
 
-// A word of two bf16 values: 2^127 for each that is no finite number, else zero
-__device__ inline uint32_t specials(uint32_t w) {
-    return ((w & 0x7f80u) == 0x7f80u ? 0x7f00u : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0x7f000000u : 0u);
-}
-
-// whether 16 values hold one that is no finite number: a NaN code or scale, or
-// a scale that can take one out of range
-__device__ inline bool has_specials(const u32x4_t& x, uint32_t s) {
-    const uint32_t nan = ((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) |
-                         ((x.z & 0x7f7f7f7fu) + 0x01010101u) | ((x.w & 0x7f7f7f7fu) + 0x01010101u);
-    return (nan & 0x80808080u) || s >= 246u;
-}
-
 template <int D, int R>
 struct Wave {
     // per row tile, lane (c, g): row c.  O: elements 16 d + 4 g ..
@@ -287,66 +295,81 @@ struct Wave {
     float pass[R];      // the score past which the reference is moved
 };
 
-// A value that is no number makes one of what sees it, and of nothing else.
+// A value that is no number makes one of what sees it, and of nothing else:
 // 2^127 in its place is multiplied with 2^127 where it is seen, and with the
-// negative: infinity, then infinity less infinity.  The rest is returned, with
-// zeros in those places.
+// negative: infinity, then infinity less infinity.  seen: as shifted for the
+// lane's positions.
 template <int D, int R>
-__device__ inline bf16x8_t take_specials(const bf16x8_t& vt, const uint32_t (&seen)[R], int d, Wave<D, R>& w) {
-    u32x4_t v = __builtin_bit_cast(u32x4_t, vt), n, m;
+__device__ inline void add_specials(const uint8_t* lds, const uint32_t (&seen)[R], Wave<D, R>& w) {
+    using T = Tile<D>;
+    const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
+    const uint16_t* bits = reinterpret_cast<const uint16_t*>(lds + T::kBits);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        n[i] = specials(v[i]);
-        m[i] = n[i] | (n[i] << 1 & 0x80008000u);
-        v[i] &= ~((n[i] & 0x4000u ? 0xffffu : 0u) | (n[i] & 0x40000000u ? 0xffff0000u : 0u));
-    }
+    for (int d = 0; d < D / 16; d++) {
+        u32x4_t n, m;
 #pragma unroll
-    for (int r = 0; r < R; r++) {
-        auto pair = [&](int k) {  // of positions k, k + 1
-            return 0x7f00u * (seen[r] >> k & 1u) | 0x7f000000u * (seen[r] >> (k + 1) & 1u);
-        };
-        const u32x4_t sees = {pair(0), pair(2), pair(16), pair(18)};
-        w.o[r][d] = mfma(__builtin_bit_cast(bf16x8_t, n), __builtin_bit_cast(bf16x8_t, sees), w.o[r][d]);
-        w.o[r][d] = mfma(__builtin_bit_cast(bf16x8_t, m), __builtin_bit_cast(bf16x8_t, sees), w.o[r][d]);
+        for (int i = 0; i < 4; i++) {  // the lane's positions 2 i, 2 i + 1 of 8
+            const int at = 16 * (i / 2) + 4 * g + 2 * (i % 2);
+            const uint32_t a = bits[at * T::kLanes + d] >> c & 1u, b = bits[(at + 1) * T::kLanes + d] >> c & 1u;
+            n[i] = 0x7f00u * a | 0x7f000000u * b;
+            m[i] = 0xff00u * a | 0xff000000u * b;
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            auto pair = [&](int k) {  // of positions k, k + 1
+                return 0x7f00u * (seen[r] >> k & 1u) | 0x7f000000u * (seen[r] >> (k + 1) & 1u);
+            };
+            const u32x4_t sees = {pair(0), pair(2), pair(16), pair(18)};
+            w.o[r][d] = mfma(__builtin_bit_cast(bf16x8_t, n), __builtin_bit_cast(bf16x8_t, sees), w.o[r][d]);
+            w.o[r][d] = mfma(__builtin_bit_cast(bf16x8_t, m), __builtin_bit_cast(bf16x8_t, sees), w.o[r][d]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
     }
-    return __builtin_bit_cast(bf16x8_t, v);
 }
 
 // A wave's part of the tile at p0, into LDS.  `special`: some of the tile's
 // positions are drafted ones or none at all; else all rows see all of them.
+// There values that are no numbers are stored as zeros, and their places kept.
 template <int D, int N>
-__device__ inline void store_part(const Seq& s, int p0, int wr, bool special, const Pages& g, Part<D, N>& r,
+__device__ inline void store_part(const Seq& s, int p0, int wr, bool special, const Halves& h, Part<D, N>& r,
                                   uint8_t* lds) {
     using T = Tile<D>;
     const int lane = threadIdx.x % kWave, key = lane / T::kLanes, piece = lane % T::kLanes;
-    bool odd = false;
 #pragma unroll
     for (int i = 0; i < N; i++) {
         const int at = (wr * N + i) * T::kKeys + key;
         *reinterpret_cast<u32x4_t*>(lds + T::code_at(at, piece)) = r.k[i];
         if (piece == 0) reinterpret_cast<typename T::scales_t*>(lds + T::kScales)[at] = r.ks[i];
-        if (special) {
-            if (!(p0 + at < s.len && ((wr * N + i) * T::kKeys >= 16 ? g.ok[1] : g.ok[0]))) {  // nothing is there
-                r.v[i] = u32x4_t{0, 0, 0, 0};
-                r.vs[i] = 0;
-            }
-            odd |= has_specials(r.v[i], r.vs[i]);
-        }
+        u32x4_t v[2];
         const float f = e8m0_as_scale(r.vs[i]);
-        bf16x8_t* v = reinterpret_cast<bf16x8_t*>(lds + at * T::kValueRow + piece * 32);
-        v[0] = decode8_e4m3(r.v[i].x, r.v[i].y, f);
-        v[1] = decode8_e4m3(r.v[i].z, r.v[i].w, f);
-    }
-    if (special) {
-        odd = __any(odd);
-        if (lane == 0) lds[T::kOdd + wr] = odd;
+        v[0] = __builtin_bit_cast(u32x4_t, decode8_e4m3(r.v[i].x, r.v[i].y, f));
+        v[1] = __builtin_bit_cast(u32x4_t, decode8_e4m3(r.v[i].z, r.v[i].w, f));
+        if (special) {
+            const bool there = p0 + at < s.len && ((wr * N + i) * T::kKeys >= 16 ? h.ok[1] : h.ok[0]);
+            uint32_t bits = 0;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                uint32_t w = there ? v[e / 4][e % 4] : 0u;
+                if ((w & 0x7f80u) == 0x7f80u) bits |= 1u << (2 * e), w &= 0xffff0000u;
+                if ((w & 0x7f800000u) == 0x7f800000u) bits |= 2u << (2 * e), w &= 0xffffu;
+                v[e / 4][e % 4] = w;
+            }
+            reinterpret_cast<uint16_t*>(lds + T::kBits)[at * T::kLanes + piece] = (uint16_t)bits;
+            const bool odd = __any(bits != 0);
+            if (lane == 0) lds[T::kOdd + wr * N + i] = odd;
+        }
+        u32x4_t* to = reinterpret_cast<u32x4_t*>(lds + at * T::kValueRow + piece * 32);
+        to[0] = v[0];
+        to[1] = v[1];
     }
 }
 
-// One step: the 32 positions from p0, whose tile is in LDS, for a wave's rows
-template <int D, int R, int WR>
-__device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R], const bf16x8_t (&q)[R][D / 32],
-                            int p0, bool special, bool ok0, bool ok1, const uint8_t* lds, Wave<D, R>& w) {
+// The weights of the 32 positions from p0, whose tile is in LDS, for a wave's
+// rows; m and with it O and its sum are moved where a score asks for it
+template <int D, int R>
+__device__ inline void weights(const AttnArgs& p, const Seq& s, const int (&node)[R], const bf16x8_t (&q)[R][D / 32],
+                               int p0, bool special, const Halves& h, const uint8_t* lds, Wave<D, R>& w,
+                               bf16x8_t (&pt)[R]) {
     using T = Tile<D>;
     const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
     f32x4_t st[2][R];
@@ -371,26 +394,11 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
             for (int r = 0; r < R; r++) st[t][r] = mfma(k1, q[r][2 * j + 1], st[t][r]);
         }
     }
-    typedef __attribute__((address_space(3))) s16x4_t lds4_t;
-    const uint8_t* column = lds + (4 * g + c / 4) * T::kValueRow + (c % 4) * 8;
-    auto value = [&](int d) {
-        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t*)(column + 32 * d));
-        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t*)(column + 16 * T::kValueRow + 32 * d));
-        const s16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        return __builtin_bit_cast(bf16x8_t, v);
-    };
-    // the first of the product's operands are on their way before the softmax
-    constexpr int kAhead = 4;
-    bf16x8_t vt[kAhead];
-#pragma unroll
-    for (int d = 0; d < kAhead; d++) vt[d] = value(d);
-
-    uint32_t seen[R];
-    bool odd = false;  // a value is no number
     if (special) {
+        uint32_t seen[R];
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            seen[r] = seen_bits(p, s, node[r], p0, ok0, ok1) >> (4 * g);
+            seen[r] = seen_bits(p, s, node[r], p0, h.ok[0], h.ok[1]) >> (4 * g);
 #pragma unroll
             for (int t = 0; t < 2; t++)
 #pragma unroll
@@ -401,8 +409,8 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
         }
         uint32_t any = 0;
 #pragma unroll
-        for (int i = 0; i < WR; i++) any |= lds[T::kOdd + i];
-        odd = uniform(any) != 0;
+        for (int i = 0; i < T::kLoads; i++) any |= lds[T::kOdd + i];
+        if (uniform(any)) add_specials<D, R>(lds, seen, w);
     }
     // the reference score, where one has passed it
     float top[R];
@@ -430,7 +438,6 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
             w.pass[r] = m + kAttnSlack / p.c;
         }
     }
-    bf16x8_t pt[R];
 #pragma unroll
     for (int r = 0; r < R; r++)
 #pragma unroll
@@ -438,13 +445,31 @@ __device__ inline void step(const AttnArgs& p, const Seq& s, const int (&node)[R
 #pragma unroll
             for (int i = 0; i < 4; i++)
                 pt[r][4 * t + i] = (__bf16)__builtin_amdgcn_exp2f(fmaf(st[t][r][i], p.c, -w.mc[r]));
+}
+
+// O and its sum with the weights of the tile in LDS
+template <int D, int R>
+__device__ inline void product(const bf16x8_t (&pt)[R], const uint8_t* lds, Wave<D, R>& w) {
+    using T = Tile<D>;
+    const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
+    typedef __attribute__((address_space(3))) s16x4_t lds4_t;
+    const uint8_t* column = lds + (4 * g + c / 4) * T::kValueRow + (c % 4) * 8;
+    auto value = [&](int d) {
+        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t*)(column + 32 * d));
+        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t*)(column + 16 * T::kValueRow + 32 * d));
+        const s16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        return __builtin_bit_cast(bf16x8_t, v);
+    };
+    constexpr int kAhead = 4;
+    bf16x8_t vt[kAhead];
+#pragma unroll
+    for (int d = 0; d < kAhead; d++) vt[d] = value(d);
     const s16x8_t one16 = {0x3f80, 0x3f80, 0x3f80, 0x3f80, 0x3f80, 0x3f80, 0x3f80, 0x3f80};
     const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, one16);
 #pragma unroll
     for (int r = 0; r < R; r++) w.sum[r] = mfma(ones, pt[r], w.sum[r]);
 #pragma unroll
     for (int d = 0; d < D / 16; d++) {
-        if (odd) vt[d % kAhead] = take_specials<D, R>(vt[d % kAhead], seen, d, w);
 #pragma unroll
         for (int r = 0; r < R; r++) w.o[r][d] = mfma(vt[d % kAhead], pt[r], w.o[r][d]);
         if (d + kAhead < D / 16) vt[d % kAhead] = value(d + kAhead);
@@ -478,7 +503,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
     __shared__ __align__(16) uint8_t buf[S::kLds];
     __shared__ float s_m[WK][ROWS], s_sum[S::kWaves][16];
     const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave), c = lane % 16, g = lane / 16;
-    const int wr = wave / WK, wk = wave % WK;
+    const int wr = wave % WR, wk = wave / WR;
     // Workgroups are dealt round the 8 XCDs; each XCD takes a run of the line, so
     // that the row tiles of a head, which read the same positions, share its L2
     const int group = (int)blockIdx.x % 8 * (p.groups / 8) + (int)blockIdx.x / 8;
@@ -512,8 +537,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
         const int32_t* table = p.a.block_table + (int64_t)b * p.a.block_table_stride;
         const int steps = stop > from ? (stop - from + 32 * WK - 1) / (32 * WK) : 0;
         int p0 = from + 32 * wk;
-        int page[2];
-        page_numbers(p, table, p0, s.len, page);
+        constexpr int kStride = 32 * WK;  // from a wave's tile to its next
+        PageRun run;
+        run.now = page_numbers(p, table, p0, kStride, s.len);
+        run.next = page_numbers(p, table, p0 + 32 * kStride, kStride, s.len);
 
         int node[R];
         bf16x8_t q[R][D / 32];
@@ -534,9 +561,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             }
         }
         Part<D, S::kParts> part;
-        Pages pages = pages_of(p, page, p0, s.len);
-        load_part(p, h, p0, wr, pages, part);
-        page_numbers(p, table, p0 + 32 * WK, s.len, page);
+        const Bases base_of_head = bases_of<D>(p.a.cache, h);
+        Halves halves = halves_of(p, run.now, 0, p0, s.len);
+        load_part(p, base_of_head, p0, wr, halves, part);
         uint8_t* qbuf = buf + wave * S::kQuery;
         auto query_at = [](int row, int piece) {  // 16-byte pieces, the 16 rows' in different banks
             return row * D * 2 + (piece ^ (D == 64 ? row / 2 : row)) * 16;
@@ -562,40 +589,48 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
         lds_barrier();
 
         uint8_t* tile = buf + S::kBuffers * wk * Tile<D>::kBytes;
-        auto is_special = [&](int at, const Pages& g) { return at + 32 > s.L || !g.ok[0] || !g.ok[1]; };
-        // the part that is to be loaded next is `ahead` tiles on
-        auto load_next = [&](int ahead) {
-            const int at = p0 + ahead * 32 * WK;
-            pages = pages_of(p, page, at, s.len);
-            load_part(p, h, at, wr, pages, part);
-            page_numbers(p, table, at + 32 * WK, s.len, page);
+        auto is_special = [&](int at, const Halves& t) { return at + 32 > s.L || !t.ok[0] || !t.ok[1]; };
+        auto load_tile = [&](int i, int at) {  // the wave's tile i, at position `at`
+            if (i % 32 == 0) {
+                run.now = run.next;
+                run.next = page_numbers(p, table, at + 32 * kStride, kStride, s.len);
+            }
+            halves = halves_of(p, run.now, i, at, s.len);
+            load_part(p, base_of_head, at, wr, halves, part);
         };
+        bf16x8_t pt[R];
         if constexpr (WR == 1) {  // a tile is its wave's own
-            for (int i = 0; i < steps && p0 < mine; i++, p0 += 32 * WK) {
-                const Pages now = pages;
+            for (int i = 0; i < steps && p0 < mine; i++, p0 += kStride) {
+                const Halves now = halves;
                 const bool special = is_special(p0, now);
                 store_part(s, p0, wr, special, now, part, tile);
                 wave_order();
-                load_next(1);
-                step<D, R, WR>(p, s, node, q, p0, special, now.ok[0], now.ok[1], tile, w);
+                load_tile(i + 1, p0 + kStride);
+                weights<D, R>(p, s, node, q, p0, special, now, tile, w, pt);
+                product<D, R>(pt, tile, w);
                 wave_order();
             }
         } else if (steps > 0) {
-            store_part(s, p0, wr, is_special(p0, pages), pages, part, tile);
-            Pages now = pages;
-            load_next(1);
+            // A step has two halves with a barrier after each.  Of the two waves
+            // of a SIMD (w and w + 4, of different tiles) one is half a step
+            // behind, so that one's softmax is beside the other's products
+            store_part(s, p0, wr, is_special(p0, halves), halves, part, tile);
+            Halves now = halves;
+            load_tile(1, p0 + kStride);
             lds_barrier();
-            for (int i = 0; i < steps; i++, p0 += 32 * WK) {
-                const Pages then = pages;
-                const int next = p0 + 32 * WK;
-                store_part(s, next, wr, is_special(next, pages), pages, part, tile + (~i & 1) * Tile<D>::kBytes);
-                load_next(2);
-                if (p0 < mine)
-                    step<D, R, WR>(p, s, node, q, p0, is_special(p0, now), now.ok[0], now.ok[1],
-                                   tile + (i & 1) * Tile<D>::kBytes, w);
-                now = then;
+            if (wave >= 4) lds_barrier();
+            for (int i = 0; i < steps; i++, p0 += kStride) {
+                const uint8_t* lds = tile + (i & 1) * Tile<D>::kBytes;
+                if (p0 < mine) weights<D, R>(p, s, node, q, p0, is_special(p0, now), now, lds, w, pt);
+                lds_barrier();
+                if (p0 < mine) product<D, R>(pt, lds, w);
+                now = halves;
+                const int next = p0 + kStride;
+                store_part(s, next, wr, is_special(next, now), now, part, tile + (~i & 1) * Tile<D>::kBytes);
+                load_tile(i + 2, p0 + 2 * kStride);
                 lds_barrier();
             }
+            if (S::kWaves > 4 && wave < 4) lds_barrier();
         }
         lds_barrier();
 
@@ -630,9 +665,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             float v[kPiece] = {}, sum = 0.f;
 #pragma unroll
             for (int i = 0; i < WK; i++) {
-                sum += s_sum[og * WK + i][orow];
+                sum += s_sum[i * WR + og][orow];
 #pragma unroll
-                for (int d = 0; d < kPiece; d++) v[d] += joined[((og * WK + i) * 16 + orow) * (D + 4) + d0 + d];
+                for (int d = 0; d < kPiece; d++) v[d] += joined[((i * WR + og) * 16 + orow) * (D + 4) + d0 + d];
             }
             if (!whole) {
                 float* dst = left + at * D + d0;
