@@ -135,7 +135,7 @@ int moe_kv_read(const moe_kv_rows_args* args, void* stream);
 typedef struct moe_tree_attention_args {
     moe_kv_cache cache;            /* head_dim 64, 128 or 256 */
     const void* q;                 /* [num_tokens, num_heads, head_dim] bf16, heads and elements contiguous */
-    int64_t q_stride;              /* elements from token to token; 0: num_heads * head_dim */
+    int64_t q_stride;              /* elements from token to token, up to 2^31; 0: num_heads * head_dim */
     void* out;                     /* as q */
     int64_t out_stride;
     const int32_t* block_table;    /* [num_seqs, max_pages] */

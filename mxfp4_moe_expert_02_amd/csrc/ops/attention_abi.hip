@@ -9,7 +9,7 @@ namespace {
 
 using moe::hip_fail;
 
-constexpr int64_t kMaxStride = 1ll << 40, kMaxPageStride = 1ll << 31, kMaxTokens = 1ll << 20, kMaxSeqs = 1ll << 16;
+constexpr int64_t kMaxStride = 1ll << 40, kMaxPageStride = 1ll << 31, kMaxTokenStride = 1ll << 31, kMaxTokens = 1ll << 20, kMaxSeqs = 1ll << 16;
 constexpr int64_t kMaxPositions = 1ll << 30, kMaxUnits = 1ll << 30;
 constexpr int kMaxHeads = 1024, kMaxMaskWords = 64;
 
@@ -74,6 +74,7 @@ int check_attention(moe_tree_attention_args* a) {
     if (a->mask ? a->mask_words < 1 || a->mask_words > kMaxMaskWords : a->mask_words != 0) return MOE_E_SHAPE;
     const int64_t row = (int64_t)a->num_heads * a->cache.head_dim;
     if (fill_stride(&a->q_stride, row) || fill_stride(&a->out_stride, row)) return MOE_E_SHAPE;
+    if (a->q_stride > kMaxTokenStride || a->out_stride > kMaxTokenStride) return MOE_E_SHAPE;
     if (T == 0 || B == 0) return MOE_OK;
     if (a->max_pages < 1 || a->max_pages > kMaxPositions / a->cache.page_size) return MOE_E_SHAPE;
     if (fill_stride(&a->block_table_stride, a->max_pages)) return MOE_E_SHAPE;

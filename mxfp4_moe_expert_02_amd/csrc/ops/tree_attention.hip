@@ -38,6 +38,7 @@ constexpr float kAttnSlack = 8.f;  // powers of two that a score may pass m by
 struct AttnArgs {
     moe_tree_attention_args a;
     int T, B, G;               // tokens, sequences, query heads per key/value head
+    uint32_t g_inverse;        // 2^32 / G, rounded up (G > 1)
     int page_shift, capacity;  // positions of a page (log2), of a sequence's table
     int groups;                // workgroups
     float c;                   // scale * log2 e
@@ -46,6 +47,11 @@ struct AttnArgs {
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
+
+// x / G for x < 2^16
+__device__ inline int by_group(const AttnArgs& p, int x) {
+    return p.G == 1 ? x : (int)__umulhi((uint32_t)x, p.g_inverse);
+}
 
 __device__ inline float minus_inf() { return -__builtin_inff(); }
 
@@ -256,6 +262,14 @@ __device__ inline void wave_order() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// The lane, anew: what is worked out from it is not kept in registers from
+// where it was worked out before (rare paths, and the ends of a row tile)
+__device__ inline int lane_again() {
+    int lane;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(lane));
+    return lane;
+}
+
 // A barrier that orders LDS alone: loads from memory stay on their way
 __device__ inline void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -302,7 +316,7 @@ struct Wave {
 template <int D, int R>
 __device__ inline void add_specials(const uint8_t* lds, const uint32_t (&seen)[R], Wave<D, R>& w) {
     using T = Tile<D>;
-    const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
+    const int lane = lane_again(), c = lane % 16, g = lane / 16;
     const uint16_t* bits = reinterpret_cast<const uint16_t*>(lds + T::kBits);
 #pragma unroll
     for (int d = 0; d < D / 16; d++) {
@@ -345,6 +359,7 @@ __device__ inline void store_part(const Seq& s, int p0, int wr, bool special, co
         v[0] = __builtin_bit_cast(u32x4_t, decode8_e4m3(r.v[i].x, r.v[i].y, f));
         v[1] = __builtin_bit_cast(u32x4_t, decode8_e4m3(r.v[i].z, r.v[i].w, f));
         if (special) {
+            const int rare = lane_again(), at = (wr * N + i) * T::kKeys + rare / T::kLanes;
             const bool there = p0 + at < s.len && ((wr * N + i) * T::kKeys >= 16 ? h.ok[1] : h.ok[0]);
             uint32_t bits = 0;
 #pragma unroll
@@ -354,7 +369,7 @@ __device__ inline void store_part(const Seq& s, int p0, int wr, bool special, co
                 if ((w & 0x7f800000u) == 0x7f800000u) bits |= 2u << (2 * e), w &= 0xffffu;
                 v[e / 4][e % 4] = w;
             }
-            reinterpret_cast<uint16_t*>(lds + T::kBits)[at * T::kLanes + piece] = (uint16_t)bits;
+            reinterpret_cast<uint16_t*>(lds + T::kBits)[at * T::kLanes + rare % T::kLanes] = (uint16_t)bits;
             const bool odd = __any(bits != 0);
             if (lane == 0) lds[T::kOdd + wr * N + i] = odd;
         }
@@ -366,9 +381,9 @@ __device__ inline void store_part(const Seq& s, int p0, int wr, bool special, co
 
 // The weights of the 32 positions from p0, whose tile is in LDS, for a wave's
 // rows; m and with it O and its sum are moved where a score asks for it
-template <int D, int R>
-__device__ inline void weights(const AttnArgs& p, const Seq& s, const int (&node)[R], const bf16x8_t (&q)[R][D / 32],
-                               int p0, bool special, const Halves& h, const uint8_t* lds, Wave<D, R>& w,
+template <int D, int R, typename Node>
+__device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, const bf16x8_t (&q)[R][D / 32], int p0,
+                               bool special, const Halves& h, const uint8_t* lds, Wave<D, R>& w,
                                bf16x8_t (&pt)[R]) {
     using T = Tile<D>;
     const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
@@ -396,9 +411,10 @@ __device__ inline void weights(const AttnArgs& p, const Seq& s, const int (&node
     }
     if (special) {
         uint32_t seen[R];
+        const int rare = lane_again();
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            seen[r] = seen_bits(p, s, node[r], p0, h.ok[0], h.ok[1]) >> (4 * g);
+            seen[r] = seen_bits(p, s, node_of(16 * r + rare % 16), p0, h.ok[0], h.ok[1]) >> (rare / 16 * 4);
 #pragma unroll
             for (int t = 0; t < 2; t++)
 #pragma unroll
@@ -502,7 +518,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
     constexpr int D = S::D, R = S::R, WR = S::WR, WK = S::WK, ROWS = S::kRows;
     __shared__ __align__(16) uint8_t buf[S::kLds];
     __shared__ float s_m[WK][ROWS], s_sum[S::kWaves][16];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave), c = lane % 16, g = lane / 16;
+    const int wave = uniform((int)threadIdx.x / kWave);
     const int wr = wave % WR, wk = wave / WR;
     // Workgroups are dealt round the 8 XCDs; each XCD takes a run of the line, so
     // that the row tiles of a head, which read the same positions, share its L2
@@ -523,17 +539,23 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             s.first = uniform(s.first), s.n = uniform(s.n), s.L = uniform(s.L), s.len = uniform(s.len);
             continue;
         }
-        const int item = (u - base) / units, u0 = (u - base) % units, u1 = min(units, u0 + end - u);
-        const int h = item / tiles, row0 = item % tiles * ROWS, rows = s.n * p.G;
+        // (unsigned: half the instructions of a signed division)
+        const uint32_t item = (uint32_t)(u - base) / (uint32_t)units;
+        const int u0 = u - base - (int)item * units, u1 = min(units, u0 + end - u);
+        const int h = (int)(item / (uint32_t)tiles), row0 = ((int)item - h * tiles) * ROWS;
+        const int here = min(ROWS, s.n * p.G - row0);  // rows of the tile
+        const int node0 = (int)((uint32_t)row0 / (uint32_t)p.G), rest = row0 - node0 * p.G;
+        // drafted token (from node0) of a row of the tile, past the last that one's
+        auto node_of = [&](int row) { return by_group(p, rest + min(row, here - 1)); };
 
         // positions that some row of the workgroup, and of the wave, may see
         const int from = u0 * kAttnUnit;
         int stop = min(s.len, u1 * kAttnUnit), mine = stop;
         if (!p.a.mask) {
-            stop = min(stop, s.L + (min(row0 + ROWS, rows) - 1) / p.G + 1);
-            mine = min(stop, s.L + (min(row0 + 16 * R * (wr + 1), rows) - 1) / p.G + 1);
+            stop = min(stop, s.L + node0 + node_of(ROWS - 1) + 1);
+            mine = min(stop, s.L + node0 + node_of(16 * R * (wr + 1) - 1) + 1);
         }
-        if (row0 + 16 * R * wr >= rows) mine = 0;
+        if (16 * R * wr >= here) mine = 0;
         const int32_t* table = p.a.block_table + (int64_t)b * p.a.block_table_stride;
         const int steps = stop > from ? (stop - from + 32 * WK - 1) / (32 * WK) : 0;
         int p0 = from + 32 * wk;
@@ -542,21 +564,21 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
         run.now = page_numbers(p, table, p0, kStride, s.len);
         run.next = page_numbers(p, table, p0 + 32 * kStride, kStride, s.len);
 
-        int node[R];
+        auto node_at = [&](int row) { return node0 + node_of(16 * R * wr + row); };  // of the wave's rows
+        const int lane = lane_again(), c = lane % 16, g = lane / 16;
         bf16x8_t q[R][D / 32];
         Wave<D, R> w;
         // the queries, whole lines at a time and through LDS (past the last row that row again)
         constexpr int kRowLanes = D / 8, kRowsAtOnce = kWave / kRowLanes;  // lanes of 16 bytes a row
+        const uint16_t* queries = (const uint16_t*)p.a.q + (int64_t)(s.first + node0) * p.a.q_stride + h * p.G * D;
         u32x4_t rows_in[R][16 / kRowsAtOnce];
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            node[r] = (min(row0 + 16 * (R * wr + r) + c, rows - 1)) / p.G;
 #pragma unroll
             for (int i = 0; i < 16 / kRowsAtOnce; i++) {
-                const int at = min(row0 + 16 * (R * wr + r) + kRowsAtOnce * i + lane / kRowLanes, rows - 1);
-                const int head = at % p.G;
-                const uint16_t* src = (const uint16_t*)p.a.q + (int64_t)(s.first + at / p.G) * p.a.q_stride +
-                                      (h * p.G + head) * D + lane % kRowLanes * 8;
+                const int row = 16 * (R * wr + r) + kRowsAtOnce * i + lane / kRowLanes, at = node_of(row);
+                const uint16_t* src = queries + (uint64_t)(uint32_t)at * (uint32_t)p.a.q_stride +
+                                      (rest + min(row, here - 1) - at * p.G) * D + lane % kRowLanes * 8;
                 rows_in[r][i] = *reinterpret_cast<const u32x4_t*>(src);
             }
         }
@@ -606,7 +628,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
                 store_part(s, p0, wr, special, now, part, tile);
                 wave_order();
                 load_tile(i + 1, p0 + kStride);
-                weights<D, R>(p, s, node, q, p0, special, now, tile, w, pt);
+                weights<D, R>(p, s, node_at, q, p0, special, now, tile, w, pt);
                 product<D, R>(pt, tile, w);
                 wave_order();
             }
@@ -621,7 +643,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             if (wave >= 4) lds_barrier();
             for (int i = 0; i < steps; i++, p0 += kStride) {
                 const uint8_t* lds = tile + (i & 1) * Tile<D>::kBytes;
-                if (p0 < mine) weights<D, R>(p, s, node, q, p0, is_special(p0, now), now, lds, w, pt);
+                if (p0 < mine) weights<D, R>(p, s, node_at, q, p0, is_special(p0, now), now, lds, w, pt);
                 lds_barrier();
                 if (p0 < mine) product<D, R>(pt, lds, w);
                 now = halves;
@@ -635,11 +657,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
         lds_barrier();
 
         // the results of the waves of a row group joined, 16 rows of each group at a time
-        if (g == 0)
+        const int own = lane_again(), oc = own % 16, og = own / 16, tid = wave * kWave + own;
+        if (og == 0)
 #pragma unroll
             for (int r = 0; r < R; r++)
-                s_m[wk][16 * (R * wr + r) + c] = w.m[r] == minus_inf() ? minus_inf() : w.mc[r];
-        __syncthreads();
+                s_m[wk][16 * (R * wr + r) + oc] = w.m[r] == minus_inf() ? minus_inf() : w.mc[r];
+        lds_barrier();
         auto top_of = [&](int row) {
             float m = s_m[0][row];
 #pragma unroll
@@ -653,21 +676,21 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
 #pragma unroll
         for (int r = 0; r < R; r++) {
             const float f = __builtin_amdgcn_exp2f((w.m[r] == minus_inf() ? minus_inf() : w.mc[r]) -
-                                                   reference(top_of(16 * (R * wr + r) + c)));
-            float* mine = joined + (wave * 16 + c) * (D + 4) + 4 * g;
+                                                   reference(top_of(16 * (R * wr + r) + oc)));
+            float* mine = joined + (wave * 16 + oc) * (D + 4) + 4 * og;
 #pragma unroll
             for (int d = 0; d < D / 16; d++)
                 *reinterpret_cast<f32x4_t*>(mine + 16 * d) = w.o[r][d] * f;
-            if (g == 0) s_sum[wave][c] = w.sum[r][0] * f;
-            __syncthreads();
-            const int og = tid / (16 * kPieces), orow = tid / kPieces % 16, d0 = tid % kPieces * kPiece;
-            const int at = 16 * (R * og + r) + orow;
+            if (og == 0) s_sum[wave][oc] = w.sum[r][0] * f;
+            lds_barrier();
+            const int of = tid / (16 * kPieces), orow = tid / kPieces % 16, d0 = tid % kPieces * kPiece;
+            const int at = 16 * (R * of + r) + orow;
             float v[kPiece] = {}, sum = 0.f;
 #pragma unroll
             for (int i = 0; i < WK; i++) {
-                sum += s_sum[i * WR + og][orow];
+                sum += s_sum[i * WR + of][orow];
 #pragma unroll
-                for (int d = 0; d < kPiece; d++) v[d] += joined[((i * WR + og) * 16 + orow) * (D + 4) + d0 + d];
+                for (int d = 0; d < kPiece; d++) v[d] += joined[((i * WR + of) * 16 + orow) * (D + 4) + d0 + d];
             }
             if (!whole) {
                 float* dst = left + at * D + d0;
@@ -677,17 +700,18 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
                     left[ROWS * D + 2 * at] = top_of(at);
                     left[ROWS * D + 2 * at + 1] = sum;
                 }
-            } else if (row0 + at < rows) {
+            } else if (at < here) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                uint16_t* dst = (uint16_t*)p.a.out + (int64_t)(s.first + (row0 + at) / p.G) * p.a.out_stride +
-                                (h * p.G + (row0 + at) % p.G) * D + d0;
+                const int node_at = node_of(at);
+                uint16_t* dst = (uint16_t*)p.a.out + (int64_t)(s.first + node0) * p.a.out_stride + h * p.G * D +
+                                (uint64_t)(uint32_t)node_at * (uint32_t)p.a.out_stride + (rest + at - node_at * p.G) * D + d0;
 #pragma unroll
                 for (int d = 0; d < kPiece; d += 4) {
                     const float o[4] = {v[d] * inv, v[d + 1] * inv, v[d + 2] * inv, v[d + 3] * inv};
                     store_piece<4>(dst + d, o);
                 }
             }
-            __syncthreads();
+            lds_barrier();
         }
         u += u1 - u0;
     }
@@ -697,7 +721,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
 // their order.  A part's weight is 2^(its reference - the largest).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinWaves * kWave) tree_attention_join_kernel(AttnArgs p) {
-    constexpr int N = D / kWave;
     const int lane = threadIdx.x % kWave;
     const int idx = uniform((int)blockIdx.x * kJoinWaves + (int)threadIdx.x / kWave);
     if (idx >= p.T * p.a.num_heads) return;
@@ -714,32 +737,45 @@ __global__ void __launch_bounds__(kJoinWaves * kWave) tree_attention_join_kernel
     auto part = [&](int i) {
         return (const float*)p.a.workspace + (2 * (int64_t)(first + i) + (i ? 0 : 1)) * p.part_floats;
     };
-    float top = minus_inf();
+    // the parts' statistics, one a lane (in turn where they are more than 64)
+    float top = minus_inf(), sum = 0.f;
     for (int i = lane; i < parts; i += kWave) top = fmaxf(top, part(i)[ROWS * D + 2 * at]);
 #pragma unroll
     for (int x = 1; x < kWave; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
     top = reference(top);
-    float v[N] = {}, sum = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += kWave) {
-        float f = 0.f, l = 0.f;
-        if (i0 + lane < parts) {
-            const float* stat = part(i0 + lane) + ROWS * D + 2 * at;
-            f = __builtin_amdgcn_exp2f(stat[0] - top);
-            l = stat[1] * f;
-        }
-        const int n = min(parts - i0, kWave);
-        for (int i = 0; i < n; i++) {
-            const float fi = __shfl(f, i);
-            sum += __shfl(l, i);
-            const float* src = part(i0 + i) + at * D + lane * N;
+    // their elements: 16 bytes a lane, kAtOnce parts at a time, kUnroll of those in flight
+    constexpr int kLanes = D / 4, kAtOnce = kWave / kLanes, kUnroll = 8;
+    const int which = lane / kLanes, e0 = lane % kLanes * 4;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < parts; i0 += kAtOnce * kUnroll) {
+        f32x4_t x[kUnroll];
+        float m[kUnroll], l[kUnroll];
 #pragma unroll
-            for (int e = 0; e < N; e++) v[e] = fmaf(src[e], fi, v[e]);
+        for (int j = 0; j < kUnroll; j++) {
+            const float* src = part(min(i0 + j * kAtOnce + which, parts - 1));
+            x[j] = *reinterpret_cast<const f32x4_t*>(src + at * D + e0);
+            m[j] = src[ROWS * D + 2 * at];
+            l[j] = src[ROWS * D + 2 * at + 1];
+        }
+#pragma unroll
+        for (int j = 0; j < kUnroll; j++) {
+            if (i0 + j * kAtOnce + which >= parts) continue;
+            const float f = __builtin_amdgcn_exp2f(m[j] - top);
+            sum = fmaf(l[j], f, sum);
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] = fmaf(x[j][e], f, v[e]);
         }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t* dst = (uint16_t*)p.a.out + (int64_t)token * p.a.out_stride + head * D + lane * N;
 #pragma unroll
-    for (int e = 0; e < N; e++) dst[e] = f32_to_bf16_rne(v[e] * inv);
+    for (int x = kLanes; x < kWave; x *= 2) {
+        sum += __shfl_xor(sum, x);
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] += __shfl_xor(v[e], x);
+    }
+    if (which) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    store_piece<4>((uint16_t*)p.a.out + (int64_t)token * p.a.out_stride + head * D + e0, o);
 }
 
 template <int D, int R, int WR, int WK>
@@ -778,6 +814,7 @@ hipError_t launch_tree_attention(const moe_tree_attention_args& a, hipStream_t s
     p.T = (int)a.num_tokens;
     p.B = (int)a.num_seqs;
     p.G = a.num_heads / a.cache.kv_heads;
+    p.g_inverse = p.G > 1 ? (uint32_t)(((1ull << 32) + p.G - 1) / p.G) : 0;
     p.page_shift = __builtin_ctz(a.cache.page_size);
     p.capacity = (int)(a.max_pages * a.cache.page_size);
     p.groups = plan.groups;
