@@ -76,9 +76,10 @@ __device__ inline int tiles_of(const AttnArgs& p, const Seq& s) {
     return (s.n * p.G + ROWS - 1) / ROWS;
 }
 __device__ inline int units_of(const Seq& s) { return max(1, (s.len + kAttnUnit - 1) / kAttnUnit); }
+// its row tiles, of all heads
 template <int ROWS>
-__device__ inline int weight_of(const AttnArgs& p, const Seq& s) {  // its units, of all heads and row tiles
-    return s.n ? tiles_of<ROWS>(p, s) * units_of(s) * p.a.cache.kv_heads : 0;
+__device__ inline int items_of(const AttnArgs& p, const Seq& s) {
+    return s.n ? tiles_of<ROWS>(p, s) * p.a.cache.kv_heads : 0;
 }
 
 // inclusive sums over the wave's lanes
@@ -95,13 +96,22 @@ __device__ inline int wave_scan(int v) {
 // All units in one line: sequence by sequence, in each its heads, in each head
 // its row tiles, in each of them its units.  Every wave works the line out
 // for itself, 64 sequences at a time, one a lane (the lengths are the device's).
+// A workgroup does `per` units of the line.  A run that goes over the end of a
+// row tile costs about as much as 4 units (its queries, the first load, the
+// join): where it lets each row tile start a run of its own by at most 3 more
+// units a run, the line is laid out so, each row tile's units rounded up to
+// whole runs (1 sequence of 9 tokens over 8192 positions: 21 -> 13 us).
 struct Line {
-    int total;  // units; 0 if the offsets are not ascending in 0 .. T
-    int per;    // units of a workgroup
+    int total;   // units; 0 if the offsets are not ascending in 0 .. T
+    int per;     // units of a workgroup
+    int round;   // a row tile's units on the line are a multiple of this
     // the last 64 sequences: the lane's, its units and those up to its end
     Seq s;
     int w, incl;
 };
+__device__ inline int on_line(int units, int round) {
+    return round == 1 ? units : (int)(((uint32_t)units + round - 1) / (uint32_t)round) * round;
+}
 template <int ROWS>
 __device__ inline void line_part(const AttnArgs& p, int b, Line* l, bool* bad) {
     l->s = read_seq(p, min(b, p.B - 1));
@@ -109,7 +119,7 @@ __device__ inline void line_part(const AttnArgs& p, int b, Line* l, bool* bad) {
         *bad = true;
         l->s.n = 0;
     }
-    l->w = b < p.B ? weight_of<ROWS>(p, l->s) : 0;
+    l->w = b < p.B ? items_of<ROWS>(p, l->s) * on_line(units_of(l->s), l->round) : 0;
     l->incl = wave_scan(l->w);
 }
 template <int ROWS>
@@ -117,6 +127,7 @@ __device__ inline Line line_of(const AttnArgs& p) {
     const int lane = threadIdx.x % kWave;
     Line l;
     l.total = 0;
+    l.round = 1;
     bool bad = false;
     for (int b0 = 0; b0 < p.B; b0 += kWave) {
         line_part<ROWS>(p, b0 + lane, &l, &bad);
@@ -124,6 +135,17 @@ __device__ inline Line line_of(const AttnArgs& p) {
     }
     if (__any(bad)) l.total = 0;
     l.per = max(1, (l.total + p.groups - 1) / p.groups);
+    if (p.B <= kWave && l.per <= 16) {
+        const int items = lane < p.B ? items_of<ROWS>(p, l.s) : 0, units = units_of(l.s);
+        for (int more = 0; more < 4; more++) {
+            const int per = l.per + more, w = items * on_line(units, per), incl = wave_scan(w);
+            const int total = __builtin_amdgcn_readlane(incl, kWave - 1);
+            if (total <= p.groups * per && l.total) {
+                l.total = total, l.per = per, l.round = per, l.w = w, l.incl = incl;
+                break;
+            }
+        }
+    }
     return l;
 }
 
@@ -505,7 +527,7 @@ struct Shape {
     static constexpr int kParts = Tile<D>::kLoads / WR;
     static_assert(kParts * WR == Tile<D>::kLoads, "a tile is dealt evenly");
     static constexpr int kBuffers = WR == 1 ? 1 : 2, kTiles = kBuffers * WK * Tile<D>::kBytes;
-    static constexpr int kResult = kWaves * 16 * (D + 4) * 4;  // at the end the waves' results, 16 rows of each
+    static constexpr int kResult = kWaves * 16 * R * (D + 4) * 4;  // at the end the waves' results
     static constexpr int kQuery = 16 * D * 2;                  // at the start 16 queries of each
     static constexpr int kLds = kTiles > kResult ? kTiles : kResult;
     static_assert(kWaves * kQuery <= kLds, "queries fit");
@@ -517,7 +539,7 @@ template <typename S>
 __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kernel(AttnArgs p) {
     constexpr int D = S::D, R = S::R, WR = S::WR, WK = S::WK, ROWS = S::kRows;
     __shared__ __align__(16) uint8_t buf[S::kLds];
-    __shared__ float s_m[WK][ROWS], s_sum[S::kWaves][16];
+    __shared__ float s_m[WK][ROWS], s_sum[WK][ROWS];
     const int wave = uniform((int)threadIdx.x / kWave);
     const int wr = wave % WR, wk = wave / WR;
     // Workgroups are dealt round the 8 XCDs; each XCD takes a run of the line, so
@@ -531,7 +553,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
     Seq s;
     int b = uniform(sequence_at<ROWS>(p, u, false, &line, &s, &base));
     while (u < end) {
-        const int tiles = tiles_of<ROWS>(p, s), units = units_of(s), all = weight_of<ROWS>(p, s);
+        const int tiles = tiles_of<ROWS>(p, s), units = units_of(s), long_units = on_line(units, line.round);
+        const int all = items_of<ROWS>(p, s) * long_units;
         if (u - base >= all) {  // on to the next sequence (there is one: u < total)
             base += all;
             b++;
@@ -540,8 +563,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             continue;
         }
         // (unsigned: half the instructions of a signed division)
-        const uint32_t item = (uint32_t)(u - base) / (uint32_t)units;
-        const int u0 = u - base - (int)item * units, u1 = min(units, u0 + end - u);
+        const uint32_t item = (uint32_t)(u - base) / (uint32_t)long_units;
+        const int u0 = u - base - (int)item * long_units, u1 = min(units, u0 + end - u);
         const int h = (int)(item / (uint32_t)tiles), row0 = ((int)item - h * tiles) * ROWS;
         const int here = min(ROWS, s.n * p.G - row0);  // rows of the tile
         const int node0 = (int)((uint32_t)row0 / (uint32_t)p.G), rest = row0 - node0 * p.G;
@@ -656,7 +679,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
         }
         lds_barrier();
 
-        // the results of the waves of a row group joined, 16 rows of each group at a time
+        // the results of the waves of a row group joined
         const int own = lane_again(), oc = own % 16, og = own / 16, tid = wave * kWave + own;
         if (og == 0)
 #pragma unroll
@@ -669,113 +692,155 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             for (int i = 1; i < WK; i++) m = fmaxf(m, s_m[i][row]);
             return m;
         };
-        const bool whole = u0 == 0 && u1 == units;
-        float* left = (float*)p.a.workspace + (2 * (int64_t)group + (u0 ? 0 : 1)) * p.part_floats;
         float* joined = reinterpret_cast<float*>(buf);
-        constexpr int kPiece = D * 16 * WR / S::kThreads, kPieces = D / kPiece;  // of a row: elements of a thread, threads
 #pragma unroll
         for (int r = 0; r < R; r++) {
             const float f = __builtin_amdgcn_exp2f((w.m[r] == minus_inf() ? minus_inf() : w.mc[r]) -
                                                    reference(top_of(16 * (R * wr + r) + oc)));
-            float* mine = joined + (wave * 16 + oc) * (D + 4) + 4 * og;
+            float* to = joined + ((wave * R + r) * 16 + oc) * (D + 4) + 4 * og;
 #pragma unroll
-            for (int d = 0; d < D / 16; d++)
-                *reinterpret_cast<f32x4_t*>(mine + 16 * d) = w.o[r][d] * f;
-            if (og == 0) s_sum[wave][oc] = w.sum[r][0] * f;
-            lds_barrier();
-            const int of = tid / (16 * kPieces), orow = tid / kPieces % 16, d0 = tid % kPieces * kPiece;
-            const int at = 16 * (R * of + r) + orow;
-            float v[kPiece] = {}, sum = 0.f;
+            for (int d = 0; d < D / 16; d++) *reinterpret_cast<f32x4_t*>(to + 16 * d) = w.o[r][d] * f;
+            if (og == 0) s_sum[wk][16 * (R * wr + r) + oc] = w.sum[r][0] * f;
+        }
+        lds_barrier();
+        const bool whole = u0 == 0 && u1 == units;
+        float* left = (float*)p.a.workspace + (2 * (int64_t)group + (u0 ? 0 : 1)) * p.part_floats;
+        uint16_t* out = (uint16_t*)p.a.out + (int64_t)(s.first + node0) * p.a.out_stride + h * p.G * D;
+        constexpr int kPiece = 8, kPieces = D / kPiece;  // elements of a thread, threads of a row
+#pragma unroll 1
+        for (int i = tid; i < ROWS * kPieces; i += S::kThreads) {
+            const int at = i / kPieces, d0 = i % kPieces * kPiece;
+            const int from_wave = at / (16 * R), from_row = at % (16 * R);
+            f32x4_t v[2] = {};
+            float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < WK; i++) {
-                sum += s_sum[i * WR + of][orow];
-#pragma unroll
-                for (int d = 0; d < kPiece; d++) v[d] += joined[((i * WR + of) * 16 + orow) * (D + 4) + d0 + d];
+            for (int k = 0; k < WK; k++) {
+                const f32x4_t* src = reinterpret_cast<const f32x4_t*>(
+                    joined + ((k * WR + from_wave) * 16 * R + from_row) * (D + 4) + d0);
+                v[0] += src[0];
+                v[1] += src[1];
+                sum += s_sum[k][at];
             }
             if (!whole) {
-                float* dst = left + at * D + d0;
-#pragma unroll
-                for (int d = 0; d < kPiece; d++) dst[d] = v[d];
+                f32x4_t* dst = reinterpret_cast<f32x4_t*>(left + at * D + d0);
+                dst[0] = v[0];
+                dst[1] = v[1];
                 if (d0 == 0) {
                     left[ROWS * D + 2 * at] = top_of(at);
                     left[ROWS * D + 2 * at + 1] = sum;
                 }
             } else if (at < here) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                const int node_at = node_of(at);
-                uint16_t* dst = (uint16_t*)p.a.out + (int64_t)(s.first + node0) * p.a.out_stride + h * p.G * D +
-                                (uint64_t)(uint32_t)node_at * (uint32_t)p.a.out_stride + (rest + at - node_at * p.G) * D + d0;
+                const int node = node_of(at);
+                float o[kPiece];
 #pragma unroll
-                for (int d = 0; d < kPiece; d += 4) {
-                    const float o[4] = {v[d] * inv, v[d + 1] * inv, v[d + 2] * inv, v[d + 3] * inv};
-                    store_piece<4>(dst + d, o);
-                }
+                for (int e = 0; e < kPiece; e++) o[e] = v[e / 4][e % 4] * inv;
+                store_piece<kPiece>(out + (uint64_t)(uint32_t)node * (uint32_t)p.a.out_stride +
+                                        (rest + at - node * p.G) * D + d0, o);
             }
-            lds_barrier();
         }
-        u += u1 - u0;
+        lds_barrier();
+        u += line.round > 1 ? line.per : u1 - u0;
     }
 }
 
-// One wave per row: the parts of a row tile that several workgroups did, in
-// their order.  A part's weight is 2^(its reference - the largest).
-template <int D, int ROWS>
+// The parts of row tiles that several workgroups did, in their order: HEADS
+// heads of a token a wave.  A part's weight is 2^(its reference - the largest).
+template <int D, int ROWS, int HEADS>
 __global__ void __launch_bounds__(kJoinWaves * kWave) tree_attention_join_kernel(AttnArgs p) {
-    const int lane = threadIdx.x % kWave;
+    const int lane = threadIdx.x % kWave, heads = p.a.num_heads, runs = (heads + HEADS - 1) / HEADS;
     const int idx = uniform((int)blockIdx.x * kJoinWaves + (int)threadIdx.x / kWave);
-    if (idx >= p.T * p.a.num_heads) return;
-    const int token = idx / p.a.num_heads, head = idx % p.a.num_heads;
+    if (idx >= p.T * runs) return;
+    const int token = (int)((uint32_t)idx / (uint32_t)runs), head0 = (idx - token * runs) * HEADS;
     Line line = line_of<ROWS>(p);
     if (line.total == 0) return;
     int base = 0;
     Seq s;
     if (sequence_at<ROWS>(p, token, true, &line, &s, &base) < 0) return;
-    const int units = units_of(s), row = (token - s.first) * p.G + head % p.G, at = row % ROWS;
-    const int u0 = base + (head / p.G * tiles_of<ROWS>(p, s) + row / ROWS) * units;
-    const int first = u0 / line.per, parts = (u0 + units - 1) / line.per - first + 1;
-    if (parts == 1) return;
-    auto part = [&](int i) {
-        return (const float*)p.a.workspace + (2 * (int64_t)(first + i) + (i ? 0 : 1)) * p.part_floats;
-    };
-    // the parts' statistics, one a lane (in turn where they are more than 64)
-    float top = minus_inf(), sum = 0.f;
-    for (int i = lane; i < parts; i += kWave) top = fmaxf(top, part(i)[ROWS * D + 2 * at]);
-#pragma unroll
-    for (int x = 1; x < kWave; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
-    top = reference(top);
-    // their elements: 16 bytes a lane, kAtOnce parts at a time, kUnroll of those in flight
-    constexpr int kLanes = D / 4, kAtOnce = kWave / kLanes, kUnroll = 8;
+    const int units = units_of(s), long_units = on_line(units, line.round), tiles = tiles_of<ROWS>(p, s);
+    // 16 bytes a lane, kAtOnce parts at a time
+    constexpr int kLanes = D / 4, kAtOnce = kWave / kLanes;
     const int which = lane / kLanes, e0 = lane % kLanes * 4;
-    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < parts; i0 += kAtOnce * kUnroll) {
-        f32x4_t x[kUnroll];
-        float m[kUnroll], l[kUnroll];
+
+    int first[HEADS], parts[HEADS], at[HEADS], most = 0;
 #pragma unroll
-        for (int j = 0; j < kUnroll; j++) {
-            const float* src = part(min(i0 + j * kAtOnce + which, parts - 1));
-            x[j] = *reinterpret_cast<const f32x4_t*>(src + at * D + e0);
-            m[j] = src[ROWS * D + 2 * at];
-            l[j] = src[ROWS * D + 2 * at + 1];
+    for (int j = 0; j < HEADS; j++) {
+        const int head = min(head0 + j, heads - 1), h = (int)((uint32_t)head / (uint32_t)p.G);
+        const int row = (token - s.first) * p.G + head - h * p.G;
+        const int u0 = base + (h * tiles + row / ROWS) * long_units;
+        at[j] = row % ROWS;
+        first[j] = (int)((uint32_t)u0 / (uint32_t)line.per);
+        parts[j] = head0 + j < heads ? (int)((uint32_t)(u0 + units - 1) / (uint32_t)line.per) - first[j] + 1 : 1;
+        most = max(most, parts[j]);
+    }
+    if (most == 1) return;
+    auto part = [&](int j, int i) {
+        return (const float*)p.a.workspace + (2 * (int64_t)(first[j] + i) + (i ? 0 : 1)) * p.part_floats;
+    };
+    // UNROLL * kAtOnce parts of COUNT heads from j0, in flight together; v and
+    // sum relative to `top`
+    auto add = [&](auto unroll, auto count, int j0, int i0, float (&top)[HEADS], f32x4_t (&v)[HEADS],
+                   float (&sum)[HEADS]) {
+        constexpr int UNROLL = decltype(unroll)::value, COUNT = decltype(count)::value;
+        f32x4_t x[COUNT][UNROLL];
+        float m[COUNT][UNROLL], l[COUNT][UNROLL];
+#pragma unroll
+        for (int j = 0; j < COUNT; j++)
+#pragma unroll
+            for (int k = 0; k < UNROLL; k++) {
+                const int i = i0 + k * kAtOnce + which;
+                const float* src = part(j0 + j, min(i, parts[j0 + j] - 1));
+                x[j][k] = *reinterpret_cast<const f32x4_t*>(src + at[j0 + j] * D + e0);
+                m[j][k] = i < parts[j0 + j] ? src[ROWS * D + 2 * at[j0 + j]] : minus_inf();
+                l[j][k] = src[ROWS * D + 2 * at[j0 + j] + 1];
+            }
+#pragma unroll
+        for (int j = 0; j < COUNT; j++) {
+            float t = top[j0 + j];
+#pragma unroll
+            for (int k = 0; k < UNROLL; k++) t = fmaxf(t, m[j][k]);
+#pragma unroll
+            for (int a = kLanes; a < kWave; a *= 2) t = fmaxf(t, __shfl_xor(t, a));
+            const float f = top[j0 + j] == minus_inf() ? 0.f : __builtin_amdgcn_exp2f(top[j0 + j] - t);
+            top[j0 + j] = t;
+            sum[j0 + j] *= f;
+            v[j0 + j] *= f;
+#pragma unroll
+            for (int k = 0; k < UNROLL; k++) {
+                if (i0 + k * kAtOnce + which >= parts[j0 + j]) continue;
+                const float g = __builtin_amdgcn_exp2f(m[j][k] - reference(t));
+                sum[j0 + j] = fmaf(l[j][k], g, sum[j0 + j]);
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[j0 + j][e] = fmaf(x[j][k][e], g, v[j0 + j][e]);
+            }
         }
+    };
+    float top[HEADS], sum[HEADS] = {};
+    f32x4_t v[HEADS] = {};
 #pragma unroll
-        for (int j = 0; j < kUnroll; j++) {
-            if (i0 + j * kAtOnce + which >= parts) continue;
-            const float f = __builtin_amdgcn_exp2f(m[j] - top);
-            sum = fmaf(l[j], f, sum);
-#pragma unroll
-            for (int e = 0; e < 4; e++) v[e] = fmaf(x[j][e], f, v[e]);
-        }
+    for (int j = 0; j < HEADS; j++) top[j] = minus_inf();
+    constexpr int kFew = 4 / kAtOnce > 0 ? 4 / kAtOnce : 1, kMany = 16 / kAtOnce;
+    if (most <= kFew * kAtOnce) {
+        add(std::integral_constant<int, kFew>{}, std::integral_constant<int, HEADS>{}, 0, 0, top, v, sum);
+    } else {
+        static_for<HEADS>([&](auto j) {
+            for (int i0 = 0; i0 < parts[j]; i0 += kMany * kAtOnce)
+                add(std::integral_constant<int, kMany>{}, std::integral_constant<int, 1>{}, j, i0, top, v, sum);
+        });
     }
 #pragma unroll
-    for (int x = kLanes; x < kWave; x *= 2) {
-        sum += __shfl_xor(sum, x);
+    for (int j = 0; j < HEADS; j++) {
 #pragma unroll
-        for (int e = 0; e < 4; e++) v[e] += __shfl_xor(v[e], x);
+        for (int a = kLanes; a < kWave; a *= 2) {
+            sum[j] += __shfl_xor(sum[j], a);
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[j][e] += __shfl_xor(v[j][e], a);
+        }
+        if (which || parts[j] == 1) continue;
+        const float inv = sum[j] == 0.f ? 0.f : 1.f / sum[j];
+        const float o[4] = {v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv};
+        store_piece<4>((uint16_t*)p.a.out + (int64_t)token * p.a.out_stride + (head0 + j) * D + e0, o);
     }
-    if (which) return;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-    store_piece<4>((uint16_t*)p.a.out + (int64_t)token * p.a.out_stride + head * D + e0, o);
 }
 
 template <int D, int R, int WR, int WK>
@@ -784,8 +849,13 @@ hipError_t launch_shape(const AttnArgs& p, hipStream_t stream) {
     tree_attention_kernel<S><<<p.groups, S::kThreads, 0, stream>>>(p);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const unsigned blocks = ((unsigned)p.T * p.a.num_heads + kJoinWaves - 1) / kJoinWaves;
-    tree_attention_join_kernel<D, S::kRows><<<blocks, kJoinWaves * kWave, 0, stream>>>(p);
+    // rows enough to fill the chip: four heads a wave, one working out of the
+    // line for them all (288 x 56 rows: 17 -> 7 us); else one
+    const bool many = (int64_t)p.T * p.a.num_heads >= 4096;
+    const int runs = many ? (p.a.num_heads + 3) / 4 : p.a.num_heads;
+    const unsigned blocks = ((unsigned)p.T * runs + kJoinWaves - 1) / kJoinWaves;
+    if (many) tree_attention_join_kernel<D, S::kRows, 4><<<blocks, kJoinWaves * kWave, 0, stream>>>(p);
+    else tree_attention_join_kernel<D, S::kRows, 1><<<blocks, kJoinWaves * kWave, 0, stream>>>(p);
     return hipGetLastError();
 }
 
