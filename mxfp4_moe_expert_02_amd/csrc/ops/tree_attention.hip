@@ -183,7 +183,7 @@ __device__ inline int sequence_at(const AttnArgs& p, int u, bool token, Line* l,
 // time (16 lanes on 16 lines, as the matrix cores' operands would have them,
 // cost 64 cycles a load in place of 16); the WR waves that share the tile take
 // kLoads / WR each.  K lies in LDS as it came, its 16-byte pieces dealt so that
-// the 16 positions of an operand read are in different banks; V lies there in
+// 8 positions of an operand read are in different banks; V lies there in
 // bf16, 16 bytes between its positions for the same reason.
 template <int D>
 struct Tile {
@@ -195,9 +195,11 @@ struct Tile {
     static constexpr int kBits = kScales + 32 * (D / 32);     // then for drafted positions a bit for each value that is
     static constexpr int kOdd = kBits + 32 * (D / 8);         // no number, then whether there are any, a byte a wave
     static constexpr int kBytes = kOdd + 16;
-    // where piece `piece` of position `key`'s codes is
+    // where piece `piece` of position `key`'s codes is: 8 neighbouring positions'
+    // in different banks; pieces 2 i and 2 i + 1 stay neighbours, and 16
+    // positions on the place is 16 D on
     __device__ static int code_at(int key, int piece) {
-        return kCodes + key * D + (piece ^ (key / (256 / D) % kLanes)) * 16;
+        return kCodes + key * D + (piece ^ (key / (256 / D) % (kLanes / 2) * 2)) * 16;
     }
 };
 
@@ -241,35 +243,31 @@ __device__ inline Halves halves_of(const AttnArgs& p, int pages, int tile, int p
     return h;
 }
 
-// What a lane's addresses start from: page 0 of a head
-struct Bases {
-    const uint8_t *k, *v, *ks, *vs;
-};
-template <int D>
-__device__ inline Bases bases_of(const moe_kv_cache& q, int h) {
-    using T = Tile<D>;
-    const uint32_t lane = threadIdx.x % kWave, key = lane / T::kLanes, piece = lane % T::kLanes;
-    const int64_t row = (int64_t)h * q.page_size;
-    return Bases{q.k_codes + row * D + lane * 16, q.v_codes + row * D + lane * 16,
-                 q.k_scales + row * (D / 32) + key * (D / 32), q.v_scales + row * (D / 32) + key * (D / 32) + piece / 2};
+// an address that is the same in all lanes, kept in scalar registers: lanes
+// add 32 bits to it
+__device__ inline const uint8_t* scalar(const uint8_t* p) {
+    uint64_t a = (uint64_t)p;
+    asm volatile("" : "+s"(a));
+    return (const uint8_t*)a;
 }
 
 template <int D, int N>
-__device__ inline void load_part(const AttnArgs& p, const Bases& base, int p0, int wr, const Halves& h,
+__device__ inline void load_part(const AttnArgs& p, int h, int p0, int wr, int lane, const Halves& halves,
                                  Part<D, N>& r) {
     using T = Tile<D>;
     const moe_kv_cache& q = p.a.cache;
+    const uint32_t key = (uint32_t)lane / T::kLanes, piece = (uint32_t)lane % T::kLanes;
 #pragma unroll
     for (int i = 0; i < N; i++) {
         const int first = (wr * N + i) * T::kKeys;
-        const uint64_t n = first >= 16 ? h.number[1] : h.number[0];
-        const uint32_t row = (p0 + first) & (q.page_size - 1);
-        const uint64_t code = n * (uint32_t)q.codes_page_stride + row * D;
-        const uint64_t scale = n * (uint32_t)q.scales_page_stride + row * (D / 32);
-        r.k[i] = *reinterpret_cast<const u32x4_t*>(base.k + code);
-        r.v[i] = *reinterpret_cast<const u32x4_t*>(base.v + code);
-        r.ks[i] = *reinterpret_cast<const typename T::scales_t*>(base.ks + scale);
-        r.vs[i] = base.vs[scale];
+        const uint64_t n = first >= 16 ? halves.number[1] : halves.number[0];
+        const uint32_t row = h * q.page_size + ((p0 + first) & (q.page_size - 1));
+        const uint64_t code = n * (uint32_t)q.codes_page_stride + (uint64_t)row * D;
+        const uint64_t scale = n * (uint32_t)q.scales_page_stride + (uint64_t)row * (D / 32);
+        r.k[i] = *reinterpret_cast<const u32x4_t*>(scalar(q.k_codes + code) + (uint32_t)lane * 16);
+        r.v[i] = *reinterpret_cast<const u32x4_t*>(scalar(q.v_codes + code) + (uint32_t)lane * 16);
+        r.ks[i] = *reinterpret_cast<const typename T::scales_t*>(scalar(q.k_scales + scale) + key * (D / 32));
+        r.vs[i] = scalar(q.v_scales + scale)[key * (D / 32) + piece / 2];
     }
 }
 
@@ -363,25 +361,25 @@ __device__ inline void add_specials(const uint8_t* lds, const uint32_t (&seen)[R
     }
 }
 
-// A wave's part of the tile at p0, into LDS.  `special`: some of the tile's
-// positions are drafted ones or none at all; else all rows see all of them.
+// A wave's part of the tile at p0, into LDS.  SPECIAL: some of the tile's
+// positions may be drafted ones or none at all; else all rows see all of them.
 // There values that are no numbers are stored as zeros, and their places kept.
-template <int D, int N>
-__device__ inline void store_part(const Seq& s, int p0, int wr, bool special, const Halves& h, Part<D, N>& r,
+template <bool SPECIAL, int D, int N>
+__device__ inline void store_part(const Seq& s, int p0, int wr, int lane, const Halves& h, Part<D, N>& r,
                                   uint8_t* lds) {
     using T = Tile<D>;
-    const int lane = threadIdx.x % kWave, key = lane / T::kLanes, piece = lane % T::kLanes;
+    const int key = lane / T::kLanes, piece = lane % T::kLanes;
 #pragma unroll
     for (int i = 0; i < N; i++) {
         const int at = (wr * N + i) * T::kKeys + key;
         *reinterpret_cast<u32x4_t*>(lds + T::code_at(at, piece)) = r.k[i];
-        if (piece == 0) reinterpret_cast<typename T::scales_t*>(lds + T::kScales)[at] = r.ks[i];
+        // (all lanes of a position: the same word to the same place)
+        reinterpret_cast<typename T::scales_t*>(lds + T::kScales)[at] = r.ks[i];
         u32x4_t v[2];
         const float f = e8m0_as_scale(r.vs[i]);
         v[0] = __builtin_bit_cast(u32x4_t, decode8_e4m3(r.v[i].x, r.v[i].y, f));
         v[1] = __builtin_bit_cast(u32x4_t, decode8_e4m3(r.v[i].z, r.v[i].w, f));
-        if (special) {
-            const int rare = lane_again(), at = (wr * N + i) * T::kKeys + rare / T::kLanes;
+        if (SPECIAL) {
             const bool there = p0 + at < s.len && ((wr * N + i) * T::kKeys >= 16 ? h.ok[1] : h.ok[0]);
             uint32_t bits = 0;
 #pragma unroll
@@ -391,7 +389,7 @@ __device__ inline void store_part(const Seq& s, int p0, int wr, bool special, co
                 if ((w & 0x7f800000u) == 0x7f800000u) bits |= 2u << (2 * e), w &= 0xffffu;
                 v[e / 4][e % 4] = w;
             }
-            reinterpret_cast<uint16_t*>(lds + T::kBits)[at * T::kLanes + rare % T::kLanes] = (uint16_t)bits;
+            reinterpret_cast<uint16_t*>(lds + T::kBits)[at * T::kLanes + piece] = (uint16_t)bits;
             const bool odd = __any(bits != 0);
             if (lane == 0) lds[T::kOdd + wr * N + i] = odd;
         }
@@ -403,12 +401,12 @@ __device__ inline void store_part(const Seq& s, int p0, int wr, bool special, co
 
 // The weights of the 32 positions from p0, whose tile is in LDS, for a wave's
 // rows; m and with it O and its sum are moved where a score asks for it
-template <int D, int R, typename Node>
+template <bool SPECIAL, int D, int R, typename Node>
 __device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, const bf16x8_t (&q)[R][D / 32], int p0,
-                               bool special, const Halves& h, const uint8_t* lds, Wave<D, R>& w,
+                               int lane, bool special, const Halves& h, const uint8_t* lds, Wave<D, R>& w,
                                bf16x8_t (&pt)[R]) {
     using T = Tile<D>;
-    const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
+    const int c = lane % 16, g = lane / 16;
     // lane (c, g): quarter g of position 16 t + c.  All reads are on their way
     // before the first is waited for (left to itself the compiler reads each
     // just before its use: 850 cycles a tile in place of 500)
@@ -422,7 +420,7 @@ __device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, 
         else ks[t] = *reinterpret_cast<const uint16_t*>(scales + 2 * g);
 #pragma unroll
         for (int j = 0; j < D / 64; j++)
-            kx[t][j] = *reinterpret_cast<const u32x4_t*>(lds + T::code_at(16 * t + c, g * (D / 64) + j));
+            kx[t][j] = *reinterpret_cast<const u32x4_t*>(lds + T::code_at(c, g * (D / 64) + j / 2 * 2) + 16 * t * D + j % 2 * 16);
     }
     __builtin_amdgcn_sched_barrier(0);
     f32x4_t st[2][R];
@@ -441,12 +439,11 @@ __device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, 
 #pragma unroll
             for (int r = 0; r < R; r++) st[t][r] = mfma(k1, q[r][2 * j + 1], st[t][r]);
         }
-    if (special) {
+    if (SPECIAL && special) {
         uint32_t seen[R];
-        const int rare = lane_again();
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            seen[r] = seen_bits(p, s, node_of(16 * r + rare % 16), p0, h.ok[0], h.ok[1]) >> (rare / 16 * 4);
+            seen[r] = seen_bits(p, s, node_of(16 * r + c), p0, h.ok[0], h.ok[1]) >> (4 * g);
 #pragma unroll
             for (int t = 0; t < 2; t++)
 #pragma unroll
@@ -497,9 +494,9 @@ __device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, 
 
 // O and its sum with the weights of the tile in LDS
 template <int D, int R>
-__device__ inline void product(const bf16x8_t (&pt)[R], const uint8_t* lds, Wave<D, R>& w) {
+__device__ inline void product(const bf16x8_t (&pt)[R], int lane, const uint8_t* lds, Wave<D, R>& w) {
     using T = Tile<D>;
-    const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
+    const int c = lane % 16, g = lane / 16;
     typedef __attribute__((address_space(3))) s16x4_t lds4_t;
     const uint8_t* column = lds + (4 * g + c / 4) * T::kValueRow + (c % 4) * 8;
     auto value = [&](int d) {
@@ -616,9 +613,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             }
         }
         Part<D, S::kParts> part;
-        const Bases base_of_head = bases_of<D>(p.a.cache, h);
         Halves halves = halves_of(p, run.now, 0, p0, s.len);
-        load_part(p, base_of_head, p0, wr, halves, part);
+        load_part(p, h, p0, wr, lane, halves, part);
         uint8_t* qbuf = buf + wave * S::kQuery;
         auto query_at = [](int row, int piece) {  // 16-byte pieces, the 16 rows' in different banks
             return row * D * 2 + (piece ^ (D == 64 ? row / 2 : row)) * 16;
@@ -645,47 +641,61 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
 
         uint8_t* tile = buf + S::kBuffers * wk * Tile<D>::kBytes;
         auto is_special = [&](int at, const Halves& t) { return at + 32 > s.L || !t.ok[0] || !t.ok[1]; };
-        auto load_tile = [&](int i, int at) {  // the wave's tile i, at position `at`
+        auto load_tile = [&](int i, int at, int lane) {  // the wave's tile i, at position `at`
             if (i % 32 == 0) {
                 run.now = run.next;
                 run.next = page_numbers(p, table, at + 32 * kStride, kStride, s.len);
             }
             halves = halves_of(p, run.now, i, at, s.len);
-            load_part(p, base_of_head, at, wr, halves, part);
+            load_part(p, h, at, wr, lane, halves, part);
         };
+        // A step: the weights and the product of tile i, the next tile stored and the
+        // one after it loaded.  Tiles that all rows see whole have a loop of
+        // their own, whose steps are one piece of code for the scheduler; the
+        // waves of a workgroup may be in either loop (a step has one barrier).
+        Halves now = halves;
         bf16x8_t pt[R];
-        if constexpr (WR == 1) {  // a tile is its wave's own
-            for (int i = 0; i < steps && p0 < mine; i++, p0 += kStride) {
-                const Halves now = halves;
-                const bool special = is_special(p0, now);
-                store_part(s, p0, wr, special, now, part, tile);
-                wave_order();
-                load_tile(i + 1, p0 + kStride);
-                weights<D, R>(p, s, node_at, q, p0, special, now, tile, w, pt);
-                product<D, R>(pt, tile, w);
-                wave_order();
-            }
-        } else if (steps > 0) {
-            // A step has two halves with a barrier after each.  Of the two waves
-            // of a SIMD (w and w + 4, of different tiles) one is half a step
-            // behind, so that one's softmax is beside the other's products
-            store_part(s, p0, wr, is_special(p0, halves), halves, part, tile);
-            Halves now = halves;
-            load_tile(1, p0 + kStride);
-            lds_barrier();
-            if (wave >= 4) lds_barrier();
-            for (int i = 0; i < steps; i++, p0 += kStride) {
-                const uint8_t* lds = tile + (i & 1) * Tile<D>::kBytes;
-                if (p0 < mine) weights<D, R>(p, s, node_at, q, p0, is_special(p0, now), now, lds, w, pt);
-                lds_barrier();
-                if (p0 < mine) product<D, R>(pt, lds, w);
+        int i = 0;
+        auto step = [&](auto special) {
+            constexpr bool SPECIAL = decltype(special)::value;
+            // the rare loop works out what comes of the lane each time, the other keeps it
+            const int lane = SPECIAL ? lane_again() : (int)threadIdx.x % kWave;
+            uint8_t* lds = tile + (WR > 1 ? (i & 1) * Tile<D>::kBytes : 0);
+            if constexpr (WR == 1) {  // a tile is its wave's own
                 now = halves;
-                const int next = p0 + kStride;
-                store_part(s, next, wr, is_special(next, now), now, part, tile + (~i & 1) * Tile<D>::kBytes);
-                load_tile(i + 2, p0 + 2 * kStride);
+                store_part<SPECIAL>(s, p0, wr, lane, now, part, lds);
+                wave_order();
+                load_tile(i + 1, p0 + kStride, lane);
+            }
+            if (!SPECIAL || p0 < mine) {
+                weights<SPECIAL, D, R>(p, s, node_at, q, p0, lane, is_special(p0, now), now, lds, w, pt);
+                product<D, R>(pt, lane, lds, w);
+            }
+            if constexpr (WR == 1) {
+                wave_order();
+            } else {
+                now = halves;
+                store_part<SPECIAL>(s, p0 + kStride, wr, lane, now, part, tile + (~i & 1) * Tile<D>::kBytes);
+                load_tile(i + 2, p0 + 2 * kStride, lane);
                 lds_barrier();
             }
-            if (S::kWaves > 4 && wave < 4) lds_barrier();
+            i++;
+            p0 += kStride;
+        };
+        if constexpr (WR == 1) {
+            while (i < steps && !is_special(p0, halves)) step(std::false_type{});
+            while (i < steps && p0 < mine) step(std::true_type{});
+        } else if (steps > 0) {
+            store_part<true>(s, p0, wr, lane, halves, part, tile);
+            load_tile(1, p0 + kStride, lane);
+            lds_barrier();
+            // (two loops one after the other would hold O in other registers each)
+            while (i < steps) {
+#pragma unroll 1
+                while (i < steps && mine && !is_special(p0, now) && !is_special(p0 + kStride, halves))
+                    step(std::false_type{});
+                if (i < steps) step(std::true_type{});
+            }
         }
         lds_barrier();
 
