@@ -12,7 +12,7 @@ import torch
 
 from . import _lib, _ops
 from ._lib import _check
-from ._ops import _BF16, _DT, _FLOATS, _FORMAT, _I32, _U8, _dev, _matrix, _row, _want
+from ._ops import _DT, _FLOATS, _FORMAT, _I32, _U8, _dev, _matrix, _row, _want
 
 ATTENTION_EXPORTED = ("moe_kv_write", "moe_kv_read", "moe_tree_attention", "moe_tree_attention_workspace")
 
@@ -50,6 +50,7 @@ def _packer(struct_type):
     return s.pack
 
 
+_I64 = (torch.int64,)
 _pack_rows = _packer(moe_kv_rows_args)
 _pack_attention = _packer(moe_tree_attention_args)
 
@@ -78,40 +79,47 @@ def _call(name, packed, dev, stream, check):
     return _check(rc, name) if check and rc else rc
 
 
-def _cache(k_codes, k_scales, v_codes, v_scales, dev):
+_u8 = torch.uint8
+
+
+def _cache(kc, ks, vc, vs, dev):
     """The cache's fields, and its [pages, kv_heads, page_size, head_dim].
     Pages may lie apart (keys' and values' alike); a page is contiguous."""
-    if k_codes.dim() != 4:
-        raise ValueError(f"k_codes: expected [pages, kv_heads, page_size, head_dim], got {tuple(k_codes.shape)}")
-    shape = pages, kv, size, D = k_codes.shape
-    strides = []
-    for t, name, s in ((k_codes, "k_codes", shape), (k_scales, "k_scales", (pages, kv, size, D // 32)),
-                       (v_codes, "v_codes", shape), (v_scales, "v_scales", (pages, kv, size, D // 32))):
-        if t.dtype != torch.uint8 or t.shape != s:
-            raise ValueError(f"{name}: expected torch.uint8 {tuple(s)}, got {t.dtype} {tuple(t.shape)}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name}: expected a tensor of the current device, got {t.device}")
-        if t.is_contiguous():
-            strides.append(s[1] * s[2] * s[3])
-        elif t.stride()[1:] == (s[2] * s[3], s[3], 1) and t.stride(0) >= s[1] * s[2] * s[3]:
-            strides.append(t.stride(0))
-        else:
-            raise ValueError(f"{name}: expected contiguous pages, got strides {t.stride()}")
-    if pages > 1 and (strides[0] != strides[2] or strides[1] != strides[3]):
-        raise ValueError(f"expected keys' and values' pages equally far apart, got {strides}")
-    return (k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), strides[0], strides[1],
-            pages, size, kv, D, 0), shape
+    shape, scales = kc.shape, ks.shape
+    if len(shape) != 4:
+        raise ValueError(f"k_codes: expected [pages, kv_heads, page_size, head_dim], got {tuple(shape)}")
+    pages, kv, size, D = shape
+    if (vc.shape != shape or vs.shape != scales or scales != (pages, kv, size, D // 32) or not (
+            kc.dtype is ks.dtype is vc.dtype is vs.dtype is _u8) or not (
+            kc.get_device() == ks.get_device() == vc.get_device() == vs.get_device() == dev)):
+        for t, name, s in ((kc, "k_codes", shape), (ks, "k_scales", (pages, kv, size, D // 32)),
+                           (vc, "v_codes", shape), (vs, "v_scales", (pages, kv, size, D // 32))):
+            if t.dtype != _u8 or t.shape != s:
+                raise ValueError(f"{name}: expected torch.uint8 {tuple(s)}, got {t.dtype} {tuple(t.shape)}")
+            if t.get_device() != dev:
+                raise ValueError(f"{name}: expected a tensor of the current device, got {t.device}")
+    n = kv * size * D
+    ld_c, ld_s = n, n // 32
+    if not (kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()):
+        for t, name, d, row in ((kc, "k_codes", D, n), (ks, "k_scales", D // 32, ld_s), (vc, "v_codes", D, n),
+                                (vs, "v_scales", D // 32, ld_s)):
+            if not t.is_contiguous() and (t.stride()[1:] != (size * d, d, 1) or t.stride(0) < row):
+                raise ValueError(f"{name}: expected contiguous pages, got strides {t.stride()}")
+        if pages > 1:
+            ld_c, ld_s = kc.stride(0), ks.stride(0)
+            if vc.stride(0) != ld_c or vs.stride(0) != ld_s:
+                raise ValueError("expected keys' and values' pages equally far apart, got strides "
+                                 f"{kc.stride()}, {vc.stride()}, {ks.stride()}, {vs.stride()}")
+    return kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), ld_c, ld_s, pages, size, kv, D, 0
 
 
-def _heads(t, name, dtypes, shape, dev):
-    """t is [tokens, heads, head_dim], tokens any distance apart: its address
-    and that distance."""
-    if t.dtype not in dtypes or t.shape != shape:
-        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    if t.get_device() != dev:
+def _heads(t, name, dtype, shape, n, dev):
+    """t is [tokens, heads, head_dim], tokens any distance apart, n the
+    elements of one: its address and that distance."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        if t.dtype != dtype or t.shape != shape:
+            raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
         raise ValueError(f"{name}: expected a tensor of the current device, got {t.device}")
-    n = shape[1] * shape[2]
     if t.is_contiguous():
         return t.data_ptr(), n
     if t.stride()[1:] != (shape[2], 1) or (shape[0] > 1 and t.stride(0) < n):
@@ -119,14 +127,20 @@ def _heads(t, name, dtypes, shape, dev):
     return t.data_ptr(), t.stride(0) if shape[0] > 1 else n
 
 
-def _rows(name, k, v, slots, cache, stream, check):
+def _rows(name, k, v, slots, kc, ks, vc, vs, stream, check):
     dev = _dev(k)
-    c, (_, kv, _, D) = _cache(*cache, dev)
-    T = slots.shape[0] if slots.dim() == 1 else -1
-    pk, ld_k = _heads(k, "k", _FLOATS, (T, kv, D), dev)
-    pv, ld_v = _heads(v, "v", (k.dtype,), (T, kv, D), dev)
-    return _call(name, _pack_rows(*c, pk, pv, ld_k, ld_v, _want(slots, "slots", (torch.int64,), (T,), dev), T,
-                                  _DT[k.dtype], 0), dev, stream, check)
+    c = _cache(kc, ks, vc, vs, dev)
+    kv, D, dtype = c[8], c[9], k.dtype
+    if dtype not in _FLOATS:
+        raise ValueError(f"k: expected {' or '.join(map(str, _FLOATS))}, got {dtype}")
+    if slots.dim() != 1:
+        raise ValueError(f"slots: expected [tokens], got {tuple(slots.shape)}")
+    T = slots.shape[0]
+    shape = (T, kv, D)
+    pk, ld_k = _heads(k, "k", dtype, shape, kv * D, dev)
+    pv, ld_v = _heads(v, "v", dtype, shape, kv * D, dev)
+    return _call(name, _pack_rows(*c, pk, pv, ld_k, ld_v, _want(slots, "slots", _I64, (T,), dev), T, _DT[dtype], 0),
+                 dev, stream, check)
 
 
 def moe_kv_write(k, v, slots, k_codes, k_scales, v_codes, v_scales, stream=None, check: bool = True) -> int:
@@ -138,13 +152,13 @@ def moe_kv_write(k, v, slots, k_codes, k_scales, v_codes, v_scales, stream=None,
     two tokens may not share one.  k_codes and v_codes [pages, kv_heads,
     page_size, head_dim], k_scales and v_scales [.., head_dim / 32] uint8 (pages
     may be strided, keys and values alike)."""
-    return _rows("moe_kv_write", k, v, slots, (k_codes, k_scales, v_codes, v_scales), stream, check)
+    return _rows("moe_kv_write", k, v, slots, k_codes, k_scales, v_codes, v_scales, stream, check)
 
 
 def moe_kv_read(k_codes, k_scales, v_codes, v_scales, slots, k, v, stream=None, check: bool = True) -> int:
     """k[t] and v[t] = the keys and values at slots[t] (tensors as for
     moe_kv_write); zeros for a slot outside the cache."""
-    return _rows("moe_kv_read", k, v, slots, (k_codes, k_scales, v_codes, v_scales), stream, check)
+    return _rows("moe_kv_read", k, v, slots, k_codes, k_scales, v_codes, v_scales, stream, check)
 
 
 def moe_tree_attention_workspace(num_tokens: int, num_seqs: int, num_heads: int, kv_heads: int,
@@ -169,12 +183,13 @@ def moe_tree_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, con
     left as they were in ``out``, one that sees nothing gets zeros.  workspace:
     a uint8 tensor of at least moe_tree_attention_workspace(...) bytes."""
     dev = _dev(q)
-    c, (_, kv, _, D) = _cache(k_codes, k_scales, v_codes, v_scales, dev)
-    if q.dim() != 3 or q.shape[2] != D:
-        raise ValueError(f"q: expected [tokens, heads, {D}], got {tuple(q.shape)}")
-    T, heads, _ = q.shape
-    pq, ld_q = _heads(q, "q", _BF16, q.shape, dev)
-    po, ld_o = _heads(out, "out", _BF16, q.shape, dev)
+    c = _cache(k_codes, k_scales, v_codes, v_scales, dev)
+    shape, D = q.shape, c[9]
+    if len(shape) != 3 or shape[2] != D:
+        raise ValueError(f"q: expected [tokens, heads, {D}], got {tuple(shape)}")
+    T, heads, _ = shape
+    pq, ld_q = _heads(q, "q", torch.bfloat16, shape, heads * D, dev)
+    po, ld_o = _heads(out, "out", torch.bfloat16, shape, heads * D, dev)
     B, pages = _matrix(block_table, "block_table", "[sequences, pages]")
     pt = _want(block_table, "block_table", _I32, (B, pages), dev, True)
     pc = _want(context_lens, "context_lens", _I32, (B,), dev)
@@ -184,7 +199,7 @@ def moe_tree_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, con
         words = _matrix(mask, "mask", "[tokens, words]")[1]
         if words < 1:  # an empty tensor has no address: not to be taken for no mask
             raise ValueError(f"mask: expected a word a token at least, got {tuple(mask.shape)}")
-        pm = _want(mask, "mask", (torch.int64,), (T, words), dev)
+        pm = _want(mask, "mask", _I64, (T, words), dev)
     if workspace is not None:
         pw, nw = _want(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel()
     return _call("moe_tree_attention", _pack_attention(*c, pq, ld_q, po, ld_o, pt, _row(block_table), pc, pf, pm,

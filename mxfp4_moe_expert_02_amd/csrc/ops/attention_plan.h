@@ -22,7 +22,7 @@ inline AttentionPlan attention_plan(int64_t T, int64_t B, int64_t heads, int64_t
     if (T <= 0 || B <= 0) return p;
     // the rows of an average sequence (the lengths are the device's)
     const int64_t rows = (T + B - 1) / B * (heads / kv_heads);
-    p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D != 256 ? 64 : 128;
+    p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D == 64 ? 64 : 128;
     p.groups = D == 256 || p.rows >= 64 ? 256 : p.rows == 16 && D == 64 ? 768 : 512;
     p.part_floats = p.rows * (D + 2);
     p.bytes = p.groups * 2 * p.part_floats * 4;

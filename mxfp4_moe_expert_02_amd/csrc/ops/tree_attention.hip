@@ -243,12 +243,15 @@ __device__ inline Halves halves_of(const AttnArgs& p, int pages, int tile, int p
     return h;
 }
 
-// an address that is the same in all lanes, kept in scalar registers: lanes
-// add 32 bits to it
-__device__ inline const uint8_t* scalar(const uint8_t* p) {
+// 32 bits of the lane's added to an address that is the same in all lanes and
+// kept in scalar registers (memory, so that the load is no flat one, which
+// would be counted among the LDS accesses)
+template <typename X>
+__device__ inline X load_at(const uint8_t* p, uint32_t offset) {
+    typedef const __attribute__((address_space(1))) uint8_t* global_t;
     uint64_t a = (uint64_t)p;
     asm volatile("" : "+s"(a));
-    return (const uint8_t*)a;
+    return *reinterpret_cast<const __attribute__((address_space(1))) X*>((global_t)a + offset);
 }
 
 template <int D, int N>
@@ -264,10 +267,10 @@ __device__ inline void load_part(const AttnArgs& p, int h, int p0, int wr, int l
         const uint32_t row = h * q.page_size + ((p0 + first) & (q.page_size - 1));
         const uint64_t code = n * (uint32_t)q.codes_page_stride + (uint64_t)row * D;
         const uint64_t scale = n * (uint32_t)q.scales_page_stride + (uint64_t)row * (D / 32);
-        r.k[i] = *reinterpret_cast<const u32x4_t*>(scalar(q.k_codes + code) + (uint32_t)lane * 16);
-        r.v[i] = *reinterpret_cast<const u32x4_t*>(scalar(q.v_codes + code) + (uint32_t)lane * 16);
-        r.ks[i] = *reinterpret_cast<const typename T::scales_t*>(scalar(q.k_scales + scale) + key * (D / 32));
-        r.vs[i] = scalar(q.v_scales + scale)[key * (D / 32) + piece / 2];
+        r.k[i] = load_at<u32x4_t>(q.k_codes + code, (uint32_t)lane * 16);
+        r.v[i] = load_at<u32x4_t>(q.v_codes + code, (uint32_t)lane * 16);
+        r.ks[i] = load_at<typename T::scales_t>(q.k_scales + scale, key * (D / 32));
+        r.vs[i] = load_at<uint8_t>(q.v_scales + scale, key * (D / 32) + piece / 2);
     }
 }
 
