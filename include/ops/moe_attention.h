@@ -161,7 +161,7 @@ int64_t moe_tree_attention_workspace(int64_t num_tokens, int64_t num_seqs, int32
 /* Pointers 16-byte aligned (context_lens, token_offsets, block_table: 4, mask:
  * 8), and so are the tokens of q and out.  MOE_E_NULL, MOE_E_SHAPE,
  * MOE_E_ALIGN, MOE_E_OPTION (scale, reserved), MOE_E_LIMIT (workspace too
- * small; or num_tokens, num_seqs, kv_heads and max_pages together past 2^31
+ * small; or num_tokens, num_seqs, kv_heads and max_pages together past 2^30
  * units of 128 positions), MOE_E_HIP. */
 int moe_tree_attention(const moe_tree_attention_args* args, void* stream);
 

@@ -50,12 +50,12 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(moe_kv_rows_args a
     uint8_t* codes = val ? a.cache.v_codes : a.cache.k_codes;
     uint8_t* scales = val ? a.cache.v_scales : a.cache.k_scales;
     const Place p = place_of(a.cache, a.slots[t]);
-    if (!p.live) return;
     codes += p.page * a.cache.codes_page_stride;
     scales += p.page * a.cache.scales_page_stride;
     for (int i = g.rows > 1 ? threadIdx.x % g.pieces : threadIdx.x; i < g.pieces; i += kKvThreads) {
         float v[8];
-        load_piece<8>(x + i * 8, v);
+        load_piece<8>(x + i * 8, v);  // (does not wait for the slot)
+        if (!p.live) return;
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);

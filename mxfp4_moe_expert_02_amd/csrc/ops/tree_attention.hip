@@ -1,23 +1,26 @@
 // tree_attention.hip -- attention of drafted tokens over the MXFP8 cache.
 //
 // The rows of one key/value head of a sequence are its drafted tokens times
-// the query heads that share it; a workgroup takes 16 R of them (a row tile)
-// over a run of positions.  Its four waves take 32 positions each in turn,
-// all rows, and keep a result of their own (m, sum, O), joined at the end of
-// the run.  Per 32 positions a wave computes
+// the query heads that share it; a workgroup takes 16, 32, 64 or 128 of them (a
+// row tile) over a run of positions.  Its waves are WR groups of 16 R rows
+// times WK that share the positions out, 32 at a time (a tile); each keeps a result of
+// its own (m, sum, O), joined at the end of the run.  Per tile a wave computes
 //
-//   S^T = K Q^T     A = K (decoded in the registers it was loaded to), B = Q
-//   P^T = 2^(c S^T - m)
-//   O^T += V^T P^T  A = V^T (decoded, through LDS), B = P^T: the lanes and
-//                   registers that S^T came in, as bf16
+//   S^T = K Q^T           A = K, decoded from its codes in LDS, B = Q
+//   P^T = 2^(c S^T - c m)
+//   O^T += V^T P^T        A = V^T (bf16 in LDS), B = P^T: the lanes and
+//                         registers that S^T came in, as bf16
 //
 // with v_mfma_f32_16x16x32_bf16.  Lane (c, g) = (l % 16, l / 16).  K's lane
-// (c, g) holds quarter g of position c's elements, which is how the cache lies
-// (one contiguous run and its scale per lane); the inner axis is then in
-// another order than the elements', and Q is loaded in the same one.  Of the 32
-// positions of O's inner axis a lane of P^T holds 4g .. 4g+3 and 16 + 4g .. ; V^T
-// comes in that order out of ds_read_b64_tr_b16, which hands a lane 4 rows of a
-// column.  The sum of the weights is one more product, with ones in V's place.
+// (c, g) holds quarter g of position c's elements, one contiguous run and its
+// scale; the inner axis is then in another order than the elements', and Q is
+// loaded in the same one.  Of the 32 positions of O's inner axis a lane of P^T
+// holds 4g .. 4g+3 and 16 + 4g .. ; V^T comes in that order out of
+// ds_read_b64_tr_b16, which hands a lane 4 rows of a column.  The sum of the
+// weights is one more product, with ones in V's place: the sum of the weights
+// as they were rounded to bf16, in float32.  (bf16 for P and V: E4M3 times a power
+// of two is exact in bf16, and P's rounding, half a step of 2^-8 a weight, is
+// that of the output.)
 //
 // m is a row's running maximum, but it is moved only where a score passes it
 // by more than 8 powers of two (P then stays below 2^8), so that most steps
@@ -27,6 +30,14 @@
 // equal run of them to each workgroup: ragged lengths cost nothing.  A row tile
 // that one workgroup does whole is finished there; else its parts go to the
 // workspace in float32 and tree_attention_join_kernel adds them in order.
+//
+// With few rows the cache's bytes bound it: 32 sequences of 9 tokens and 56
+// heads (8 of keys) over up to 16384 positions of 128 elements take 182 us, 4.1 TB/s;
+// 64 of 1 token over up to 8000 of 64 elements 78 us, 4.3 TB/s.  With
+// many it is the waves' own work: 8 trees of up to 64 tokens over up to 16001
+// positions take 148 us, 551 TFLOP/s, in which the exponentials, the decoding of K
+// and the products each have a third, and the two waves of a SIMD, which
+// meet at a barrier each tile, overlap little of it.
 #include "attention_internal.h"
 
 namespace moe {
@@ -100,7 +111,7 @@ __device__ inline int wave_scan(int v) {
 // row tile costs about as much as 4 units (its queries, the first load, the
 // join): where it lets each row tile start a run of its own by at most 3 more
 // units a run, the line is laid out so, each row tile's units rounded up to
-// whole runs (1 sequence of 9 tokens over 8192 positions: 21 -> 13 us).
+// whole runs (1 sequence of 9 tokens over 8192 positions: 27 -> 20 us).
 struct Line {
     int total;   // units; 0 if the offsets are not ascending in 0 .. T
     int per;     // units of a workgroup
@@ -542,7 +553,7 @@ struct Shape {
     static constexpr int kLds = kTiles > kResult ? kTiles : kResult;
     static_assert(kWaves * kQuery <= kLds, "queries fit");
     // waves per SIMD that the registers and LDS leave room for
-    static constexpr int kPerSimd = D == 256 ? 1 : D == 64 && R == 1 ? 3 : 2;
+    static constexpr int kPerSimd = D == 256 ? 1 : 2;
 };
 
 template <typename S>
@@ -654,8 +665,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
         };
         // A step: the weights and the product of tile i, the next tile stored and the
         // one after it loaded.  Tiles that all rows see whole have a loop of
-        // their own, whose steps are one piece of code for the scheduler; the
-        // waves of a workgroup may be in either loop (a step has one barrier).
+        // their own, whose steps are one piece of code for the scheduler (8 trees
+        // of 64 tokens: 155 -> 148 us); the waves of a workgroup may be in either
+        // loop (a step has one barrier).
         Halves now = halves;
         bf16x8_t pt[R];
         int i = 0;
