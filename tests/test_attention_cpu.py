@@ -138,3 +138,15 @@ def test_workspace_sizes(A):
                 for D in (64, 128, 256):
                     # within 1024 results of 80 rows, whatever the lengths
                     assert 0 < f(T, B, heads, kv, D) <= 1024 * 80 * 4 * (D + 4), (T, B, heads, kv, D)
+
+
+@pytest.mark.parametrize("name", ["moe_kv_write", "moe_kv_read", "moe_tree_attention"])
+def test_far_strides(A, name):
+    """Pages, and tokens of queries, may lie 2^31 apart and no further."""
+    from mxfp4_moe_expert_02_amd import MOE_E_HIP, MOE_E_SHAPE
+    call = (lambda **kw: _attend(A, **kw)) if name == "moe_tree_attention" else (lambda **kw: _rows(A, name, **kw))
+    over = ["codes_page_stride", "scales_page_stride"] + ["q_stride", "out_stride"] * (name == "moe_tree_attention")
+    for field in over:
+        assert call(**{field: (1 << 31) + 16}) == MOE_E_SHAPE, field
+        if not gpu_available():
+            assert call(**{field: 1 << 31}) == MOE_E_HIP, field

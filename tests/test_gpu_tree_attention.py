@@ -424,6 +424,74 @@ def test_graph(M):
         lens = [min(400, lens[0] + 3), lens[1] + 9, lens[2] + 4]
 
 
+@pytest.mark.parametrize("heads,kv,D,page,seqs", [
+    (56, 8, 128, 64, [(300, 30), (700, 31), (20, 20)]), (7, 1, 128, 16, [(200, 60), (330, 60)] * 5),
+    (13, 1, 64, 32, [(600, 200), (100, 150)]), (6, 2, 256, 16, [(260, 40)] * 18), (64, 4, 64, 16, [(500, 5)] * 14)])
+def test_parts_of_many_rows(M, heads, kv, D, page, seqs):
+    """Rows enough that a wave joins the parts of several heads, numbers of
+    heads that are not a multiple of those."""
+    say(f"attention of many rows heads={heads} kv={kv} D={D} seqs={seqs[:2]}")
+    b = Batch(M, seqs, heads, kv, D, page, pad=1, seed=heads)
+    assert b.T * heads >= 4096
+    b.call()
+    b.check("out")
+
+
+@pytest.mark.parametrize("heads,kv,D,n", [
+    (8, 8, 128, 1), (12, 4, 64, 1), (4, 4, 256, 1), (16, 4, 128, 7), (16, 4, 64, 7), (16, 4, 256, 7), (14, 2, 128, 9),
+    (14, 2, 64, 9), (14, 2, 256, 9), (14, 2, 128, 12), (14, 2, 256, 12)])
+def test_long_runs_of_a_shared_prefix(M, heads, kv, D, n):
+    """Sequences whose tables name the same pages up to their drafted tokens,
+    and so many of them that a workgroup goes through long runs of positions,
+    over the ends of sequences and over a page that is none.  Every eleventh
+    sequence is compared."""
+    import torch
+    say(f"attention behind a shared prefix heads={heads} kv={kv} D={D} n={n}")
+    rng = np.random.default_rng(D + n)
+    page, B, L = 32, 64, 8032
+    own = 1 if n <= page else 2
+    held = L // page
+    cache = A.Cache(held + B * own, kv, page, D, seed=n)
+    draw = lambda m: rng.standard_normal((m, kv, D)).astype(np.float32).astype(np.float64)
+    prefix = []
+    for which in "kv":
+        codes, scales = _encode(draw(L))
+        cache.put(which, np.arange(L), codes, scales)
+        prefix.append(R.mx8_values(codes, scales))
+    table = np.concatenate([np.broadcast_to(np.arange(held), (B, held)),
+                            held + np.arange(B * own).reshape(B, own)], 1).astype(np.int32)
+    drafted = {"k": {}, "v": {}}
+    for b in range(B):
+        for which in "kv":
+            codes, scales = _encode(draw(n))
+            pos = np.arange(L, L + n)
+            cache.put(which, table[b, pos // page].astype(np.int64) * page + pos % page, codes, scales)
+            drafted[which][b] = R.mx8_values(codes, scales)
+    lost = {11: held - 2, 33: 150, 55: 0}           # a page of these sequences is none
+    for b, at in lost.items():
+        table[b, at] = held + B * own + at
+    mask = _tree(rng, n, 1, empty=0.0)
+    q = R.tensor(rng.standard_normal((B * n, heads, D)), "bf16")
+    out = torch.full_like(q, 9)
+    i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+    ws = torch.randint(0, 256, (M.moe_tree_attention_workspace(B * n, B, heads, kv, D),), dtype=torch.uint8,
+                       device="cuda")
+    scale = 1.0 / np.sqrt(D)
+    M.moe_tree_attention(q, *cache.tensors, i32(table), i32([L] * B), i32(np.arange(B + 1) * n), out, scale,
+                         mask=torch.from_numpy(np.tile(mask, (B, 1)).view(np.int64)).cuda(), workspace=ws)
+    torch.cuda.synchronize()
+    got, qv = R.values(out), R.values(q)
+    for b in range(0, B, 11):
+        k, v = (np.concatenate([p, drafted[w][b]]) for p, w in zip(prefix, "kv"))
+        gone = np.arange(lost[b] * page, lost[b] * page + page) if b in lost else []
+        for i in (0, n - 1):
+            at = np.setdiff1d(A.seen(L, n, mask[i], i), gone)
+            for h in range(heads):
+                g = h // (heads // kv)
+                o, err, _ = A.attend(qv[b * n + i, h], k[at, g], v[at, g], scale)
+                R.assert_between(got[b * n + i, h], R.bf16_rne(o - err), R.bf16_rne(o + err), f"sequence {b}, {i}")
+
+
 def test_binding_refuses(M):
     import torch
     b = Batch(M, [(20, 4), (30, 3)], 4, 2, 64, 16, tree=True)
