@@ -146,7 +146,7 @@ __device__ inline Line line_of(const AttnArgs& p) {
     }
     if (__any(bad)) l.total = 0;
     l.per = max(1, (l.total + p.groups - 1) / p.groups);
-    if (p.B <= kWave && l.per <= 16) {
+    if (p.B <= kWave && l.per <= 1024) {  // (past that it does not matter, and w might overflow)
         const int items = lane < p.B ? items_of<ROWS>(p, l.s) : 0, units = units_of(l.s);
         for (int more = 0; more < 4; more++) {
             const int per = l.per + more, w = items * on_line(units, per), incl = wave_scan(w);
