@@ -18,9 +18,9 @@
 // holds 4g .. 4g+3 and 16 + 4g .. ; V^T comes in that order out of
 // ds_read_b64_tr_b16, which hands a lane 4 rows of a column.  The sum of the
 // weights is one more product, with ones in V's place: the sum of the weights
-// as they were rounded to bf16, in float32.  (bf16 for P and V: E4M3 times a power
-// of two is exact in bf16, and P's rounding, half a step of 2^-8 a weight, is
-// that of the output.)
+// as they were rounded to bf16, in float32.  (bf16 for K, P and V: E4M3 times a
+// power of two is exact in bf16, and P's rounding, off by at most 2^-8 of a
+// weight, is that of the output.)
 //
 // m is a row's running maximum, but it is moved only where a score passes it
 // by more than 8 powers of two (P then stays below 2^8), so that most steps
@@ -35,9 +35,10 @@
 // heads (8 of keys) over up to 16384 positions of 128 elements take 182 us, 4.1 TB/s;
 // 64 of 1 token over up to 8000 of 64 elements 78 us, 4.3 TB/s.  With
 // many it is the waves' own work: 8 trees of up to 64 tokens over up to 16001
-// positions take 148 us, 551 TFLOP/s, in which the exponentials, the decoding of K
-// and the products each have a third, and the two waves of a SIMD, which
-// meet at a barrier each tile, overlap little of it.
+// positions take 148 us, 551 TFLOP/s.  Per tile a wave has 34 matrix
+// instructions (544 cycles), 16 exponentials (256), 88 other vector instructions
+// (350) and 65 scalar ones; the two waves of a SIMD take 2900 cycles for a
+// tile each: they overlap little of it (the matrix cores are busy 25 %).
 #include "attention_internal.h"
 
 namespace moe {
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(kJoinWaves * kWave) tree_attention_join_kernel
     int first[HEADS], parts[HEADS], at[HEADS], most = 0;
 #pragma unroll
     for (int j = 0; j < HEADS; j++) {
-        const int head = min(head0 + j, heads - 1), h = (int)((uint32_t)head / (uint32_t)p.G);
+        const int head = min(head0 + j, heads - 1), h = by_group(p, head);
         const int row = (token - s.first) * p.G + head - h * p.G;
         const int u0 = base + (h * tiles + row / ROWS) * long_units;
         at[j] = row % ROWS;
@@ -885,7 +886,7 @@ hipError_t launch_shape(const AttnArgs& p, hipStream_t stream) {
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     // rows enough to fill the chip: four heads a wave, one working out of the
-    // line for them all (288 x 56 rows: 17 -> 7 us); else one
+    // line for them all (288 x 56 rows: 17 -> 9 us); else one
     const bool many = (int64_t)p.T * p.a.num_heads >= 4096;
     const int runs = many ? (p.a.num_heads + 3) / 4 : p.a.num_heads;
     const unsigned blocks = ((unsigned)p.T * runs + kJoinWaves - 1) / kJoinWaves;
