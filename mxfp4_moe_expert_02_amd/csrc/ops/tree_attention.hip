@@ -255,34 +255,54 @@ __device__ inline Halves halves_of(const AttnArgs& p, int pages, int tile, int p
     return h;
 }
 
-// 32 bits of the lane's added to an address that is the same in all lanes and
+// 32 bits of the lane's, and a constant, added to an address that is the same in all lanes and
 // kept in scalar registers (memory, so that the load is no flat one, which
 // would be counted among the LDS accesses)
 template <typename X>
-__device__ inline X load_at(const uint8_t* p, uint32_t offset) {
+__device__ inline X load_at(const uint8_t* p, uint32_t offset, int more) {
     typedef const __attribute__((address_space(1))) uint8_t* global_t;
     uint64_t a = (uint64_t)p;
     asm volatile("" : "+s"(a));
-    return *reinterpret_cast<const __attribute__((address_space(1))) X*>((global_t)a + offset);
+    return *reinterpret_cast<const __attribute__((address_space(1))) X*>((global_t)a + offset + more);
 }
 
-template <int D, int N>
-__device__ inline void load_part(const AttnArgs& p, int h, int p0, int wr, int lane, const Halves& halves,
-                                 Part<D, N>& r) {
-    using T = Tile<D>;
+// Where a wave's part of a tile is: its codes and scales in the tile's first and
+// second half (only one of them where waves share the tile, WR > 1: the same
+// then).  The addresses are worked out well before the loads, while the tile
+// before is waited for in LDS: beside the loads they cost 400 to 600 cycles
+// a step.
+struct Source {
+    const uint8_t *k[2], *v[2], *ks[2], *vs[2];
+};
+template <int D, int WR>
+__device__ inline Source source_of(const AttnArgs& p, int h, int p0, int wr, const Halves& halves) {
     const moe_kv_cache& q = p.a.cache;
-    const uint32_t key = (uint32_t)lane / T::kLanes, piece = (uint32_t)lane % T::kLanes;
+    Source r;
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        const int first = (wr * N + i) * T::kKeys;
+    for (int t = 0; t < (WR == 1 ? 2 : 1); t++) {
+        const int first = WR == 1 ? 16 * t : 32 / WR * wr;
         const uint64_t n = first >= 16 ? halves.number[1] : halves.number[0];
         const uint32_t row = h * q.page_size + ((p0 + first) & (q.page_size - 1));
         const uint64_t code = n * (uint32_t)q.codes_page_stride + (uint64_t)row * D;
         const uint64_t scale = n * (uint32_t)q.scales_page_stride + (uint64_t)row * (D / 32);
-        r.k[i] = load_at<u32x4_t>(q.k_codes + code, (uint32_t)lane * 16);
-        r.v[i] = load_at<u32x4_t>(q.v_codes + code, (uint32_t)lane * 16);
-        r.ks[i] = load_at<typename T::scales_t>(q.k_scales + scale, key * (D / 32));
-        r.vs[i] = load_at<uint8_t>(q.v_scales + scale, key * (D / 32) + piece / 2);
+        r.k[t] = q.k_codes + code, r.v[t] = q.v_codes + code;
+        r.ks[t] = q.k_scales + scale, r.vs[t] = q.v_scales + scale;
+    }
+    return r;
+}
+
+template <int D, int WR, int N>
+__device__ inline void load_part(const Source& from, int lane, Part<D, N>& r) {
+    using T = Tile<D>;
+    const uint32_t key = (uint32_t)lane / T::kLanes, piece = (uint32_t)lane % T::kLanes;
+    constexpr int kOfHalf = WR == 1 ? N / 2 : N;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int t = i / kOfHalf, on = (i - t * kOfHalf) * T::kKeys;  // positions into the half
+        r.k[i] = load_at<u32x4_t>(from.k[t], (uint32_t)lane * 16, on * D);
+        r.v[i] = load_at<u32x4_t>(from.v[t], (uint32_t)lane * 16, on * D);
+        r.ks[i] = load_at<typename T::scales_t>(from.ks[t], key * (D / 32), on * (D / 32));
+        r.vs[i] = load_at<uint8_t>(from.vs[t], key * (D / 32) + piece / 2, on * (D / 32));
     }
 }
 
@@ -415,11 +435,12 @@ __device__ inline void store_part(const Seq& s, int p0, int wr, int lane, const 
 }
 
 // The weights of the 32 positions from p0, whose tile is in LDS, for a wave's
-// rows; m and with it O and its sum are moved where a score asks for it
-template <bool SPECIAL, int D, int R, typename Node>
+// rows; m and with it O and its sum are moved where a score asks for it.
+// meanwhile: what is done while the keys are waited for.
+template <bool SPECIAL, int D, int R, typename Node, typename Meanwhile>
 __device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, const bf16x8_t (&q)[R][D / 32], int p0,
                                int lane, bool special, const Halves& h, const uint8_t* lds, Wave<D, R>& w,
-                               bf16x8_t (&pt)[R]) {
+                               bf16x8_t (&pt)[R], Meanwhile&& meanwhile) {
     using T = Tile<D>;
     const int c = lane % 16, g = lane / 16;
     // lane (c, g): quarter g of position 16 t + c.  All reads are on their way
@@ -438,6 +459,7 @@ __device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, 
             kx[t][j] = *reinterpret_cast<const u32x4_t*>(lds + T::code_at(c, g * (D / 64) + j / 2 * 2) + 16 * t * D + j % 2 * 16);
     }
     __builtin_amdgcn_sched_barrier(0);
+    meanwhile();
     f32x4_t st[2][R];
 #pragma unroll
     for (int t = 0; t < 2; t++)
@@ -629,7 +651,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
         }
         Part<D, S::kParts> part;
         Halves halves = halves_of(p, run.now, 0, p0, s.len);
-        load_part(p, h, p0, wr, lane, halves, part);
+        load_part<D, WR>(source_of<D, WR>(p, h, p0, wr, halves), lane, part);
         uint8_t* qbuf = buf + wave * S::kQuery;
         auto query_at = [](int row, int piece) {  // 16-byte pieces, the 16 rows' in different banks
             return row * D * 2 + (piece ^ (D == 64 ? row / 2 : row)) * 16;
@@ -656,22 +678,23 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
 
         uint8_t* tile = buf + S::kBuffers * wk * Tile<D>::kBytes;
         auto is_special = [&](int at, const Halves& t) { return at + 32 > s.L || !t.ok[0] || !t.ok[1]; };
-        auto load_tile = [&](int i, int at, int lane) {  // the wave's tile i, at position `at`
+        Halves now = halves, next;  // of tile i, of the one after that in `part` (which has halves)
+        auto source = [&](int i, int at) {  // of the wave's tile i, at position `at`
             if (i % 32 == 0) {
                 run.now = run.next;
                 run.next = page_numbers(p, table, at + 32 * kStride, kStride, s.len);
             }
-            halves = halves_of(p, run.now, i, at, s.len);
-            load_part(p, h, at, wr, lane, halves, part);
+            next = halves_of(p, run.now, i, at, s.len);
+            return source_of<D, WR>(p, h, at, wr, next);
         };
         // A step: the weights and the product of tile i, the next tile stored and the
         // one after it loaded.  Tiles that all rows see whole have a loop of
         // their own, whose steps are one piece of code for the scheduler (8 trees
         // of 64 tokens: 155 -> 148 us); the waves of a workgroup may be in either
         // loop (a step has one barrier).
-        Halves now = halves;
         bf16x8_t pt[R];
         int i = 0;
+        Source ahead = source(1, p0 + kStride);  // of the tile after that in `part`
         auto step = [&](auto special) {
             constexpr bool SPECIAL = decltype(special)::value;
             // the rare loop works out what comes of the lane each time, the other keeps it
@@ -681,18 +704,23 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
                 now = halves;
                 store_part<SPECIAL>(s, p0, wr, lane, now, part, lds);
                 wave_order();
-                load_tile(i + 1, p0 + kStride, lane);
+                halves = next;
+                load_part<D, WR>(ahead, lane, part);
             }
+            auto meanwhile = [&] { ahead = source(i + 2, p0 + 2 * kStride); };
             if (!SPECIAL || p0 < mine) {
-                weights<SPECIAL, D, R>(p, s, node_at, q, p0, lane, is_special(p0, now), now, lds, w, pt);
+                weights<SPECIAL, D, R>(p, s, node_at, q, p0, lane, is_special(p0, now), now, lds, w, pt, meanwhile);
                 product<D, R>(pt, lane, lds, w);
+            } else {
+                meanwhile();
             }
             if constexpr (WR == 1) {
                 wave_order();
             } else {
                 now = halves;
                 store_part<SPECIAL>(s, p0 + kStride, wr, lane, now, part, tile + (~i & 1) * Tile<D>::kBytes);
-                load_tile(i + 2, p0 + 2 * kStride, lane);
+                halves = next;
+                load_part<D, WR>(ahead, lane, part);
                 lds_barrier();
             }
             i++;
@@ -703,7 +731,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             while (i < steps && p0 < mine) step(std::true_type{});
         } else if (steps > 0) {
             store_part<true>(s, p0, wr, lane, halves, part, tile);
-            load_tile(1, p0 + kStride, lane);
+            halves = next;
+            load_part<D, WR>(ahead, lane, part);
             lds_barrier();
             // (two loops one after the other would hold O in other registers each)
             while (i < steps) {
