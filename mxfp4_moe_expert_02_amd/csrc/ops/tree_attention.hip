@@ -32,13 +32,13 @@
 // workspace in float32 and tree_attention_join_kernel adds them in order.
 //
 // With few rows the cache's bytes bound it: 32 sequences of 9 tokens and 56
-// heads (8 of keys) over up to 16384 positions of 128 elements take 182 us, 4.1 TB/s;
+// heads (8 of keys) over up to 16384 positions of 128 elements take 178 us, 4.1 TB/s;
 // 64 of 1 token over up to 8000 of 64 elements 78 us, 4.3 TB/s.  With
 // many it is the waves' own work: 8 trees of up to 64 tokens over up to 16001
-// positions take 148 us, 551 TFLOP/s.  Per tile a wave has 34 matrix
+// positions take 141 us, 577 TFLOP/s.  Per tile a wave has 34 matrix
 // instructions (544 cycles), 16 exponentials (256), 88 other vector instructions
-// (350) and 65 scalar ones; the two waves of a SIMD take 2900 cycles for a
-// tile each: they overlap little of it (the matrix cores are busy 25 %).
+// (350) and 65 scalar ones; the two waves of a SIMD take 2700 cycles for a
+// tile each: they overlap little of it (the matrix cores are busy 26 %).
 #include "attention_internal.h"
 
 namespace moe {
@@ -270,7 +270,7 @@ __device__ inline X load_at(const uint8_t* p, uint32_t offset, int more) {
 // second half (only one of them where waves share the tile, WR > 1: the same
 // then).  The addresses are worked out well before the loads, while the tile
 // before is waited for in LDS: beside the loads they cost 400 to 600 cycles
-// a step.
+// a step (8 trees of 64 tokens: 149 -> 141 us).
 struct Source {
     const uint8_t *k[2], *v[2], *ks[2], *vs[2];
 };
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
         // A step: the weights and the product of tile i, the next tile stored and the
         // one after it loaded.  Tiles that all rows see whole have a loop of
         // their own, whose steps are one piece of code for the scheduler (8 trees
-        // of 64 tokens: 155 -> 148 us); the waves of a workgroup may be in either
+        // of 64 tokens: 155 -> 149 us); the waves of a workgroup may be in either
         // loop (a step has one barrier).
         bf16x8_t pt[R];
         int i = 0;
