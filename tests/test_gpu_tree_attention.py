@@ -492,6 +492,19 @@ def test_long_runs_of_a_shared_prefix(M, heads, kv, D, n):
                 R.assert_between(got[b * n + i, h], R.bf16_rne(o - err), R.bf16_rne(o + err), f"sequence {b}, {i}")
 
 
+@pytest.mark.parametrize("count", [63, 64, 65, 129])
+@pytest.mark.parametrize("heads,kv,D", [(7, 1, 128), (4, 2, 256)])
+def test_numbers_of_sequences(M, count, heads, kv, D):
+    """As many sequences as a wave's lanes, fewer and more, the first and the
+    last of them without tokens."""
+    say(f"attention of {count} sequences D={D}")
+    rng = np.random.default_rng(count)
+    seqs = [(int(rng.integers(0, 150)), int(rng.integers(0, 3)) * int(0 < i < count - 1)) for i in range(count)]
+    b = Batch(M, seqs, heads, kv, D, 16, tree=count % 2 == 0, pad=2, lead=1, seed=count)
+    b.call()
+    b.check("out")
+
+
 def test_binding_refuses(M):
     import torch
     b = Batch(M, [(20, 4), (30, 3)], 4, 2, 64, 16, tree=True)
