@@ -396,12 +396,15 @@ __device__ inline void add_specials(const uint8_t* lds, const uint32_t (&seen)[R
     }
 }
 
-// A wave's part of the tile at p0, into LDS.  SPECIAL: some of the tile's
-// positions may be drafted ones or none at all; else all rows see all of them.
-// There values that are no numbers are stored as zeros, and their places kept.
+// A wave's part of the tile at p0, into LDS.  special: some of the tile's
+// positions are drafted ones or none at all; else all rows see all of them.
+// There values that are no numbers are stored as zeros, and their places kept:
+// `weights` puts them back, which goes by the same question of the same tile.
+// The waves that share a tile have the same answer, whichever loop each is
+// in.  (SPECIAL false: a loop that knows it is not.)
 template <bool SPECIAL, int D, int N>
-__device__ inline void store_part(const Seq& s, int p0, int wr, int lane, const Halves& h, Part<D, N>& r,
-                                  uint8_t* lds) {
+__device__ inline void store_part(const Seq& s, int p0, int wr, int lane, bool special, const Halves& h,
+                                  Part<D, N>& r, uint8_t* lds) {
     using T = Tile<D>;
     const int key = lane / T::kLanes, piece = lane % T::kLanes;
 #pragma unroll
@@ -414,7 +417,7 @@ __device__ inline void store_part(const Seq& s, int p0, int wr, int lane, const 
         const float f = e8m0_as_scale(r.vs[i]);
         v[0] = __builtin_bit_cast(u32x4_t, decode8_e4m3(r.v[i].x, r.v[i].y, f));
         v[1] = __builtin_bit_cast(u32x4_t, decode8_e4m3(r.v[i].z, r.v[i].w, f));
-        if (SPECIAL) {
+        if (SPECIAL && special) {
             const bool there = p0 + at < s.len && ((wr * N + i) * T::kKeys >= 16 ? h.ok[1] : h.ok[0]);
             uint32_t bits = 0;
 #pragma unroll
@@ -702,7 +705,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             uint8_t* lds = tile + (WR > 1 ? (i & 1) * Tile<D>::kBytes : 0);
             if constexpr (WR == 1) {  // a tile is its wave's own
                 now = halves;
-                store_part<SPECIAL>(s, p0, wr, lane, now, part, lds);
+                store_part<SPECIAL>(s, p0, wr, lane, is_special(p0, now), now, part, lds);
                 wave_order();
                 halves = next;
                 load_part<D, WR>(ahead, lane, part);
@@ -718,7 +721,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
                 wave_order();
             } else {
                 now = halves;
-                store_part<SPECIAL>(s, p0 + kStride, wr, lane, now, part, tile + (~i & 1) * Tile<D>::kBytes);
+                store_part<SPECIAL>(s, p0 + kStride, wr, lane, is_special(p0 + kStride, now), now, part,
+                                    tile + (~i & 1) * Tile<D>::kBytes);
                 halves = next;
                 load_part<D, WR>(ahead, lane, part);
                 lds_barrier();
@@ -730,7 +734,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
             while (i < steps && !is_special(p0, halves)) step(std::false_type{});
             while (i < steps && p0 < mine) step(std::true_type{});
         } else if (steps > 0) {
-            store_part<true>(s, p0, wr, lane, halves, part, tile);
+            store_part<true>(s, p0, wr, lane, is_special(p0, halves), halves, part, tile);
             halves = next;
             load_part<D, WR>(ahead, lane, part);
             lds_barrier();
