@@ -115,8 +115,12 @@ int moe_kv_read(const moe_kv_rows_args* args, void* stream);
  *   out[i, h] = sum_p w_p v_p,   w = softmax over the p it sees of scale * <q[i, h], k_p>
  *
  * zeros if it sees none.  What a token does not see has no part in its
- * result, whatever it holds.  Tokens of no sequence (before the first offset,
- * behind the last) have no result: their rows of `out` are left as they were.
+ * result, whatever it holds.  A NaN in a value that it sees makes one of that
+ * element of its result; an infinite value (one beyond float32's range) makes
+ * an infinity of its sign, a NaN where there are both signs, and may make one
+ * where its weight is below 2^-126.  Tokens of no sequence (before the first
+ * offset, behind the last) have no result: their rows of `out` are left as
+ * they were.
  *
  * Products and sums are float32's (of bf16 factors that hold q, k and v
  * exactly; a cached value below 2^-126 may count as zero, one beyond

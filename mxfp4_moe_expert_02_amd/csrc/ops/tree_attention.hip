@@ -204,8 +204,8 @@ struct Tile {
     static constexpr int kValueRow = 2 * D + 16;              // bytes of a position's values in LDS
     static constexpr int kCodes = 32 * kValueRow;             // V, then K from here,
     static constexpr int kScales = kCodes + 32 * D;           // then K's scales,
-    static constexpr int kBits = kScales + 32 * (D / 32);     // then for drafted positions a bit for each value that is
-    static constexpr int kOdd = kBits + 32 * (D / 8);         // no number, then whether there are any, a byte a wave
+    static constexpr int kBits = kScales + 32 * (D / 32);     // then for special tiles a bit for each value that is infinite
+    static constexpr int kOdd = kBits + 32 * (D / 8);         // or no number, then whether there are any, a byte a load
     static constexpr int kBytes = kOdd + 16;
     // where piece `piece` of position `key`'s codes is: 8 neighbouring positions'
     // in different banks; pieces 2 i and 2 i + 1 stay neighbours, and 16
@@ -364,10 +364,11 @@ struct Wave {
     float pass[R];      // the score past which the reference is moved
 };
 
-// A value that is no number makes one of what sees it, and of nothing else:
-// 2^127 in its place is multiplied with 2^127 where it is seen, and with the
-// negative: infinity, then infinity less infinity.  seen: as shifted for the
-// lane's positions.
+// A value that is infinite or no number makes one of what sees it, and of
+// nothing else (0 times it would): in its place 2^127 is multiplied with 2^127
+// where it is seen, or the negative, or for no number both: infinity less
+// infinity.  Which it is the value's place holds (`store_part`).  For an O that
+// is not scaled by 0 any more.  seen: as shifted for the lane's positions.
 template <int D, int R>
 __device__ inline void add_specials(const uint8_t* lds, const uint32_t (&seen)[R], Wave<D, R>& w) {
     using T = Tile<D>;
@@ -380,8 +381,11 @@ __device__ inline void add_specials(const uint8_t* lds, const uint32_t (&seen)[R
         for (int i = 0; i < 4; i++) {  // the lane's positions 2 i, 2 i + 1 of 8
             const int at = 16 * (i / 2) + 4 * g + 2 * (i % 2);
             const uint32_t a = bits[at * T::kLanes + d] >> c & 1u, b = bits[(at + 1) * T::kLanes + d] >> c & 1u;
-            n[i] = 0x7f00u * a | 0x7f000000u * b;
-            m[i] = 0xff00u * a | 0xff000000u * b;
+            const uint8_t* value = lds + at * T::kValueRow + (16 * d + c) * 2;
+            const uint32_t va = *reinterpret_cast<const uint16_t*>(value);
+            const uint32_t vb = *reinterpret_cast<const uint16_t*>(value + T::kValueRow);
+            n[i] = 0x7f00u * (va != 0x8000u ? a : 0u) | 0x7f000000u * (vb != 0x8000u ? b : 0u);
+            m[i] = 0xff00u * (va != 0 ? a : 0u) | 0xff000000u * (vb != 0 ? b : 0u);
         }
 #pragma unroll
         for (int r = 0; r < R; r++) {
@@ -398,8 +402,9 @@ __device__ inline void add_specials(const uint8_t* lds, const uint32_t (&seen)[R
 
 // A wave's part of the tile at p0, into LDS.  special: some of the tile's
 // positions are drafted ones or none at all; else all rows see all of them.
-// There values that are no numbers are stored as zeros, and their places kept:
-// `weights` puts them back, which goes by the same question of the same tile.
+// There values that are infinite or no numbers are stored without their
+// exponent (+0, -0, or for no number something small that is not 0), and their
+// places kept: `weights` puts them back, by the same question of the same tile.
 // The waves that share a tile have the same answer, whichever loop each is
 // in.  (SPECIAL false: a loop that knows it is not.)
 template <bool SPECIAL, int D, int N>
@@ -423,8 +428,8 @@ __device__ inline void store_part(const Seq& s, int p0, int wr, int lane, bool s
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 uint32_t w = there ? v[e / 4][e % 4] : 0u;
-                if ((w & 0x7f80u) == 0x7f80u) bits |= 1u << (2 * e), w &= 0xffff0000u;
-                if ((w & 0x7f800000u) == 0x7f800000u) bits |= 2u << (2 * e), w &= 0xffffu;
+                if ((w & 0x7f80u) == 0x7f80u) bits |= 1u << (2 * e), w &= ~0x7f80u;
+                if ((w & 0x7f800000u) == 0x7f800000u) bits |= 2u << (2 * e), w &= ~0x7f800000u;
                 v[e / 4][e % 4] = w;
             }
             reinterpret_cast<uint16_t*>(lds + T::kBits)[at * T::kLanes + piece] = (uint16_t)bits;
@@ -479,8 +484,8 @@ __device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, 
 #pragma unroll
             for (int r = 0; r < R; r++) st[t][r] = mfma(k1, q[r][2 * j + 1], st[t][r]);
         }
+    uint32_t seen[R];
     if (SPECIAL && special) {
-        uint32_t seen[R];
 #pragma unroll
         for (int r = 0; r < R; r++) {
             seen[r] = seen_bits(p, s, node_of(16 * r + c), p0, h.ok[0], h.ok[1]) >> (4 * g);
@@ -492,10 +497,6 @@ __device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, 
                     st[t][r][i] = __uint_as_float((__float_as_uint(st[t][r][i]) & keep) | (0xff800000u & ~keep));
                 }
         }
-        uint32_t any = 0;
-#pragma unroll
-        for (int i = 0; i < T::kLoads; i++) any |= lds[T::kOdd + i];
-        if (uniform(any)) add_specials<D, R>(lds, seen, w);
     }
     // the reference score, where one has passed it
     float top[R];
@@ -522,6 +523,12 @@ __device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, 
             w.mc[r] = mc;
             w.pass[r] = m + kAttnSlack / p.c;
         }
+    }
+    if (SPECIAL && special) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < T::kLoads; i++) any |= lds[T::kOdd + i];
+        if (uniform(any)) add_specials<D, R>(lds, seen, w);
     }
 #pragma unroll
     for (int r = 0; r < R; r++)

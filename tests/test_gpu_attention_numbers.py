@@ -145,10 +145,51 @@ def test_block_without_a_scale(M, D, G, counts):
         M.moe_kv_read(*s.cache.tensors, slots, k, v)
         v[0, 0, 40] = float("inf")
         M.moe_kv_write(k, v, slots, *s.cache.tensors)
-        got = s.call()
         want = plain.copy()
         for b in range(len(counts)):
             want[s.seers(b, position), 0, :, 32:64] = np.nan
-        np.testing.assert_array_equal(got, want, err_msg=str(position))
+        np.testing.assert_array_equal(s.call(), want, err_msg=str(position))
+        # a scale that is none makes NaN of every code, not infinities
+        s.cache.vc[page, 0, offset, 32:64] = torch.arange(32, device="cuda").byte() * 8 + 4
+        np.testing.assert_array_equal(s.call(), want, err_msg=f"codes at {position}")
         for t, was in zip(s.cache.tensors, keep):
             t[page] = was
+
+
+@pytest.mark.parametrize("D,G,counts", SHAPES, ids=str)
+def test_infinite_values_in_any_tile(M, D, G, counts):
+    """A value beyond float32's range is an infinity of its sign for what sees
+    it, whether its tile holds committed positions alone, drafted ones or a page
+    that is none; two of different signs, or one beside a NaN, make a NaN."""
+    say(f"attention with infinite cached values D={D} G={G} counts={counts}")
+    s = Shared(M, D, 2, G, counts, {b: p for b, p in LOST.items() if b < len(counts)}, seed=D + len(counts))
+    spots = s.spots()
+    # their blocks: zeros under the largest scale, 448 2^127 being no float32
+    for b, position in spots:
+        page, offset = s.place(b or 0, position)
+        s.cache.vc[page, s.kv - 1, offset] = 0
+        s.cache.vs[page, s.kv - 1, offset] = 254
+    plain = s.call()
+    assert np.isfinite(plain).all()
+    keep = s.cache.vc.clone()
+    # one infinity an element
+    want = plain.copy()
+    for tokens, d, code in s.put(spots, [0x7e, 0xfe, 0xfe, 0x7e, 0x7e] * len(spots)):
+        want[tokens, -1, :, d] = -np.inf if code & 0x80 else np.inf
+    np.testing.assert_array_equal(s.call(), want)
+    # several in one element: of one sign, of both, beside a NaN
+    for n, codes in ((5, [0x7e] * 5), (5, [0xfe] * 5), (6, [0x7e] * 5 + [0xfe]), (4, [0x7f, 0x7e, 0x7e, 0x7e]),
+                     (len(spots), [0xfe] * (len(spots) - 1) + [0x7e])):
+        s.cache.vc.copy_(keep)
+        some = spots[-n:]
+        seen = np.zeros((2, s.T), bool)     # tokens that see a value above, below zero (a NaN: both)
+        for (b, position), code in zip(some, codes):
+            page, offset = s.place(b or 0, position)
+            s.cache.vc[page, s.kv - 1, offset, 17] = code
+            tokens = sum((s.seers(q, position) for q in (range(len(counts)) if b is None else [b])), [])
+            seen[0, tokens] |= code in (0x7e, 0x7f)
+            seen[1, tokens] |= code in (0xfe, 0x7f)
+        want = plain.copy()
+        for above, below, value in ((True, False, np.inf), (False, True, -np.inf), (True, True, np.nan)):
+            want[(seen[0] == above) & (seen[1] == below), -1, :, 17] = value
+        np.testing.assert_array_equal(s.call(), want, err_msg=str(codes))
