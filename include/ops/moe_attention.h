@@ -147,7 +147,7 @@ typedef struct moe_tree_attention_args {
     const int32_t* context_lens;   /* [num_seqs] */
     const int32_t* token_offsets;  /* [num_seqs + 1] */
     const uint64_t* mask;          /* [num_tokens, mask_words] or NULL */
-    int64_t mask_words;            /* 1 .. 64; 0 with mask == NULL */
+    int64_t mask_words;            /* 1 .. 64; 0 with mask == NULL (without tokens or sequences 0 .. 64) */
     void* workspace;               /* at least moe_tree_attention_workspace() bytes */
     int64_t workspace_bytes;
     int64_t num_tokens;            /* 0 .. 2^20, of q and out */

@@ -71,11 +71,12 @@ int check_attention(moe_tree_attention_args* a) {
     if ((rc = check_attention_sizes(T, B, a->num_heads, a->cache.kv_heads, a->cache.head_dim)) != MOE_OK) return rc;
     // what a score is multiplied by, in powers of two, is a normal number too
     if (!(a->scale > 0.f) || !isnormal(a->scale) || !isnormal(a->scale * 1.4426950408889634f)) return MOE_E_OPTION;
-    if (a->mask ? a->mask_words < 1 || a->mask_words > kMaxMaskWords : a->mask_words != 0) return MOE_E_SHAPE;
+    if (a->mask_words < 0 || a->mask_words > kMaxMaskWords) return MOE_E_SHAPE;
     const int64_t row = (int64_t)a->num_heads * a->cache.head_dim;
     if (fill_stride(&a->q_stride, row) || fill_stride(&a->out_stride, row)) return MOE_E_SHAPE;
     if (a->q_stride > kMaxTokenStride || a->out_stride > kMaxTokenStride) return MOE_E_SHAPE;
     if (T == 0 || B == 0) return MOE_OK;
+    if ((a->mask != nullptr) != (a->mask_words != 0)) return MOE_E_SHAPE;  // (an empty mask has no address)
     if (a->max_pages < 1 || a->max_pages > kMaxPositions / a->cache.page_size) return MOE_E_SHAPE;
     if (fill_stride(&a->block_table_stride, a->max_pages)) return MOE_E_SHAPE;
     if (!a->q || !a->out || !a->block_table || !a->context_lens || !a->token_offsets) return MOE_E_NULL;

@@ -150,3 +150,16 @@ def test_far_strides(A, name):
         assert call(**{field: (1 << 31) + 16}) == MOE_E_SHAPE, field
         if not gpu_available():
             assert call(**{field: 1 << 31}) == MOE_E_HIP, field
+
+
+def test_nothing_to_do_with_a_mask(A):
+    """No tokens, or no sequences: an empty mask has no address, and the words
+    of its rows are no reason to refuse."""
+    from mxfp4_moe_expert_02_amd import MOE_E_SHAPE, MOE_OK
+    for empty in (dict(num_tokens=0), dict(num_seqs=0)):
+        for words in (0, 1, 2, 64):
+            for mask in (0, 0xa000):
+                assert _attend(A, q=0, out=0, workspace=0, workspace_bytes=0, mask=mask, mask_words=words,
+                               **empty) == MOE_OK, (empty, mask, words)
+        for words in (-1, 65):
+            assert _attend(A, mask=0, mask_words=words, **empty) == MOE_E_SHAPE

@@ -523,3 +523,18 @@ def test_binding_refuses(M):
             M.moe_tree_attention(*good, **bad)
     assert (b.out == 9).all()
     assert M.moe_tree_attention(b.qt[:0], *b.cache.tensors, b.table_t, b.ctx_t, b.off_t, b.out[:0], 1.0) == M.MOE_OK
+
+
+def test_empty_batch(M):
+    """A call without tokens, or without sequences, is one that does nothing,
+    with a mask and without."""
+    import torch
+    b = Batch(M, [(20, 4), (30, 3)], 4, 2, 64, 16, tree=True)
+    for mask in (b.mask_t, None):
+        kw = dict(mask=None if mask is None else mask[:0], workspace=b.ws)
+        none = torch.zeros_like(b.off_t)
+        assert M.moe_tree_attention(b.qt[:0], *b.cache.tensors, b.table_t, b.ctx_t, none, b.out[:0], 1.0, **kw) == M.MOE_OK
+        assert M.moe_tree_attention(b.qt, *b.cache.tensors, b.table_t[:0], b.ctx_t[:0], none[:1], b.out, 1.0, mask=mask,
+                                    workspace=b.ws[:0]) == M.MOE_OK
+    torch.cuda.synchronize()
+    assert (b.out == 9).all()
