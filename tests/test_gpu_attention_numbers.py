@@ -193,3 +193,46 @@ def test_infinite_values_in_any_tile(M, D, G, counts):
         for above, below, value in ((True, False, np.inf), (False, True, -np.inf), (True, True, np.nan)):
             want[(seen[0] == above) & (seen[1] == below), -1, :, 17] = value
         np.testing.assert_array_equal(s.call(), want, err_msg=str(codes))
+
+
+@pytest.mark.parametrize("D,G,counts", [s for s in SHAPES if max(s[2]) > 1], ids=str)
+def test_rows_do_not_touch_each_other(M, D, G, counts):
+    """A token's result keeps its bits whatever its siblings ask for, and
+    whatever the drafted keys and values that it does not see are: over several
+    tiles a wave, with scores that rise again and again."""
+    say(f"attention with siblings changed D={D} G={G} counts={counts}")
+    s = Shared(M, D, 2, G, counts, {b: p for b, p in LOST.items() if b < len(counts)}, seed=2 * D + sum(counts))
+    s.q.mul_(3)
+    plain = s.call()
+    query, mask = s.q.clone(), s.mask.copy()
+    # the second token of each sequence asks for something else, louder and louder
+    odd = s.offsets[:-1][np.array(counts) > 1] + 1
+    others = np.setdiff1d(np.arange(s.T), odd)
+    for factor in (-1, 0.01, 4, 30):
+        s.q.copy_(query)
+        s.q[odd] *= factor
+        got = s.call()
+        assert np.array_equal(got[others], plain[others]), factor
+        assert not np.array_equal(got[odd], plain[odd])
+    # a head alone, beside the other heads of its rows
+    s.q.copy_(query)
+    s.q[:, G] *= 20
+    got = s.call()
+    assert np.array_equal(np.delete(got, 0, 2)[:, 1], np.delete(plain, 0, 2)[:, 1])
+    assert np.array_equal(got[:, 0], plain[:, 0])
+    s.q.copy_(query)
+    # drafted keys and values as large as any, of which each only its own token sees
+    changed = False
+    for b, n in enumerate(counts):
+        for j in range(n):
+            if s.seers(b, CONTEXT + j) not in ([], [s.offsets[b] + j]):
+                continue
+            page, offset = s.place(b, CONTEXT + j)
+            for t in (s.cache.ks, s.cache.vs):
+                t[page, :, offset] = 140
+            got = s.call()
+            others = np.setdiff1d(np.arange(s.T), s.seers(b, CONTEXT + j))
+            assert np.array_equal(got[others], plain[others]), (b, j)
+            plain[s.seers(b, CONTEXT + j)] = got[s.seers(b, CONTEXT + j)]
+            changed = True
+    assert changed
