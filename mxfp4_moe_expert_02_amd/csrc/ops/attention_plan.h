@@ -51,4 +51,24 @@ inline int64_t attention_most_units(int64_t T, int64_t B, int64_t heads, int64_t
     return tiles * kv_heads * ((positions + kAttnUnit - 1) / kAttnUnit);
 }
 
+// The launch that joins the parts: a wave takes one head of a token, or four
+// where the rows are enough to fill the chip (one working out of the line for
+// them all; 288 x 56 rows: 17 -> 9 us).  Its workgroups in rows of kJoinRow: a
+// grid's dimension holds less than 2^32 threads, and 2^28 rows come to that.
+constexpr int kJoinWaves = 4;  // of a workgroup
+constexpr int64_t kJoinRow = 1 << 20;
+struct AttentionJoin {
+    int heads;      // of a wave
+    unsigned x, y;  // workgroups
+};
+
+inline AttentionJoin attention_join(int64_t T, int64_t heads) {
+    AttentionJoin j{};
+    j.heads = T * heads >= 4096 ? 4 : 1;
+    const int64_t waves = T * ((heads + j.heads - 1) / j.heads), groups = (waves + kJoinWaves - 1) / kJoinWaves;
+    j.x = (unsigned)(groups < kJoinRow ? groups : kJoinRow);
+    j.y = (unsigned)((groups + kJoinRow - 1) / kJoinRow);
+    return j;
+}
+
 }  // namespace moe

@@ -44,7 +44,6 @@
 namespace moe {
 namespace {
 
-constexpr int kJoinWaves = 4;
 constexpr float kAttnSlack = 8.f;  // powers of two that a score may pass m by
 
 struct AttnArgs {
@@ -827,7 +826,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSimd) tree_attention_kerne
 template <int D, int ROWS, int HEADS>
 __global__ void __launch_bounds__(kJoinWaves * kWave) tree_attention_join_kernel(AttnArgs p) {
     const int lane = threadIdx.x % kWave, heads = p.a.num_heads, runs = (heads + HEADS - 1) / HEADS;
-    const int idx = uniform((int)blockIdx.x * kJoinWaves + (int)threadIdx.x / kWave);
+    const int idx = uniform(((int)blockIdx.y * (int)kJoinRow + (int)blockIdx.x) * kJoinWaves + (int)threadIdx.x / kWave);
     if (idx >= p.T * runs) return;
     const int token = (int)((uint32_t)idx / (uint32_t)runs), head0 = (idx - token * runs) * HEADS;
     Line line = line_of<ROWS>(p);
@@ -927,13 +926,10 @@ hipError_t launch_shape(const AttnArgs& p, hipStream_t stream) {
     tree_attention_kernel<S><<<p.groups, S::kThreads, 0, stream>>>(p);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    // rows enough to fill the chip: four heads a wave, one working out of the
-    // line for them all (288 x 56 rows: 17 -> 9 us); else one
-    const bool many = (int64_t)p.T * p.a.num_heads >= 4096;
-    const int runs = many ? (p.a.num_heads + 3) / 4 : p.a.num_heads;
-    const unsigned blocks = ((unsigned)p.T * runs + kJoinWaves - 1) / kJoinWaves;
-    if (many) tree_attention_join_kernel<D, S::kRows, 4><<<blocks, kJoinWaves * kWave, 0, stream>>>(p);
-    else tree_attention_join_kernel<D, S::kRows, 1><<<blocks, kJoinWaves * kWave, 0, stream>>>(p);
+    const AttentionJoin join = attention_join(p.T, p.a.num_heads);
+    const dim3 grid(join.x, join.y);
+    if (join.heads == 4) tree_attention_join_kernel<D, S::kRows, 4><<<grid, kJoinWaves * kWave, 0, stream>>>(p);
+    else tree_attention_join_kernel<D, S::kRows, 1><<<grid, kJoinWaves * kWave, 0, stream>>>(p);
     return hipGetLastError();
 }
 

@@ -538,3 +538,28 @@ def test_empty_batch(M):
                                     workspace=b.ws[:0]) == M.MOE_OK
     torch.cuda.synchronize()
     assert (b.out == 9).all()
+
+
+def test_rows_beyond_one_grid(M):
+    """2^28 rows of queries (more threads than a grid's dimension holds, and far
+    past 32 bits of elements), nearly all of no sequence."""
+    import torch
+    say("attention of 2^28 rows of queries")
+    heads, D, T = 1024, 64, 1 << 18
+    b = Batch(M, [(300, 5)], heads, 1, D, 16, tree=True, seed=12)
+    b.call()
+    b.check("small")
+    q = torch.empty(T, heads, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 9)
+    q[T - 7:T - 2] = b.qt
+    mask = torch.zeros(T, 1, dtype=torch.int64, device="cuda")
+    mask[T - 7:T - 2] = b.mask_t
+    ws = torch.empty(M.moe_tree_attention_workspace(T, 1, heads, 1, D), dtype=torch.uint8, device="cuda")
+    assert M.moe_tree_attention(q, *b.cache.tensors, b.table_t, b.ctx_t, b.off_t + (T - 7), out, b.scale, mask=mask,
+                                workspace=ws) == M.MOE_OK
+    torch.cuda.synchronize()
+    assert torch.equal(out[T - 7:T - 2], b.out)
+    for rest in (out[:100], out[T // 2:T // 2 + 100], out[T - 100:T - 7], out[T - 2:]):
+        assert (rest == 9).all()
+    del q, out, rest
+    torch.cuda.empty_cache()
