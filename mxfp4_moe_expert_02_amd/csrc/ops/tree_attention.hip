@@ -510,19 +510,20 @@ __device__ inline void weights(const AttnArgs& p, const Seq& s, Node&& node_of, 
     if (__any(passed)) {
 #pragma unroll
         for (int r = 0; r < R; r++) {
+#pragma clang fp contract(off)
             float t = top[r];
             t = fmaxf(t, __shfl_xor(t, 16));
             t = fmaxf(t, __shfl_xor(t, 32));
-            // (a row whose own has not passed keeps it: its result does not depend on the others)
-            const bool moved = t > w.pass[r];
-            const float mc = moved ? t * p.c : w.mc[r];
-            const float f = !moved ? 1.f : w.m[r] == minus_inf() ? 0.f : __builtin_amdgcn_exp2f(w.mc[r] - mc);
+            // (a row whose own has not passed keeps it, and f is 1, as c m is rounded
+            // alike each time: its result does not depend on the other rows)
+            const float m = t > w.pass[r] ? t : w.m[r], mc = m == minus_inf() ? 0.f : m * p.c;
+            const float f = w.m[r] == minus_inf() ? 0.f : __builtin_amdgcn_exp2f(w.mc[r] - mc);
 #pragma unroll
             for (int d = 0; d < D / 16; d++) w.o[r][d] *= f;
             w.sum[r] *= f;
-            w.m[r] = moved ? t : w.m[r];
+            w.m[r] = m;
             w.mc[r] = mc;
-            w.pass[r] = moved ? t + kAttnSlack / p.c : w.pass[r];
+            w.pass[r] = m + kAttnSlack / p.c;
         }
     }
     if (SPECIAL && special) {
