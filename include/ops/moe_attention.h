@@ -62,7 +62,7 @@ typedef struct moe_kv_cache {
     int64_t num_pages;          /* 1 .. 2^31 - 1 */
     int32_t page_size;          /* 16, 32, 64, .. 1024 */
     int32_t kv_heads;           /* 1 .. 1024 */
-    int32_t head_dim;           /* a multiple of 32, 32 .. 512 */
+    int32_t head_dim;           /* a multiple of 32, 32 .. 512 (moe_tree_attention: 64, 128 or 256) */
     int32_t reserved;           /* 0 */
 } moe_kv_cache;
 
@@ -123,8 +123,8 @@ int moe_kv_read(const moe_kv_rows_args* args, void* stream);
  * they were.
  *
  * Products and sums are float32's (of bf16 factors that hold q, k and v
- * exactly; a cached value below 2^-126 may count as zero, one beyond
- * float32's range as infinite); the weights e^(s - m) are rounded to bf16 for
+ * exactly; a query or a cached value below 2^-126 may count as zero, one
+ * beyond float32's range counts as infinite); the weights e^(s - m) are rounded to bf16 for
  * the product with v, and the sum they are divided by is that of the rounded
  * ones.  m is the running maximum as it last was where a score passed it by
  * more than 8 powers of two.  Sums are added in an order that the sizes and
@@ -158,7 +158,8 @@ typedef struct moe_tree_attention_args {
 } moe_tree_attention_args;
 
 /* Bytes of workspace (0 without tokens or sequences), or a negative status
- * for sizes that moe_tree_attention refuses. */
+ * for sizes that moe_tree_attention refuses.  Of the call's own sizes: fewer
+ * sequences with more tokens each may need more. */
 int64_t moe_tree_attention_workspace(int64_t num_tokens, int64_t num_seqs, int32_t num_heads, int32_t kv_heads,
                                      int32_t head_dim);
 

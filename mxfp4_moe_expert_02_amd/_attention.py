@@ -151,7 +151,8 @@ def moe_kv_write(k, v, slots, k_codes, k_scales, v_codes, v_scales, stream=None,
     position; a token whose slot is outside the cache (-1) is not written, and
     two tokens may not share one.  k_codes and v_codes [pages, kv_heads,
     page_size, head_dim], k_scales and v_scales [.., head_dim / 32] uint8 (pages
-    may be strided, keys and values alike)."""
+    may be strided, keys and values alike).  head_dim is a multiple of 32 up to
+    512; moe_tree_attention takes 64, 128 and 256."""
     return _rows("moe_kv_write", k, v, slots, k_codes, k_scales, v_codes, v_scales, stream, check)
 
 
@@ -180,8 +181,9 @@ def moe_tree_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, con
     those whose bit is set in its row of mask [T, words] int64 (bit j % 64 of
     word j / 64), or without a mask those up to its own.  block_table [B, pages],
     context_lens [B] and token_offsets [B + 1] int32.  Tokens of no sequence are
-    left as they were in ``out``, one that sees nothing gets zeros.  workspace:
-    a uint8 tensor of at least moe_tree_attention_workspace(...) bytes."""
+    left as they were in ``out``, one that sees nothing gets zeros.  head_dim is
+    64, 128 or 256.  workspace: a uint8 tensor of at least
+    moe_tree_attention_workspace(...) bytes for the call's own sizes."""
     dev = _dev(q)
     c = _cache(k_codes, k_scales, v_codes, v_scales, dev)
     shape, D = q.shape, c[9]

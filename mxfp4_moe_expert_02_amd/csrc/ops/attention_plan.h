@@ -23,20 +23,27 @@ inline AttentionPlan attention_plan(int64_t T, int64_t B, int64_t heads, int64_t
     // The rows of an average sequence (the lengths are the device's), in as few
     // tiles as they fit: a tile reads and decodes its positions anew.  7 query
     // heads a key/value head, over 8000 positions, of 16 / 32 / 64 / 128 rows:
-    //   32 sequences of 4 tokens (28 rows)  D 64:   71 /  53 /  75 us
-    //                                       D 128: 125 /  93 / 112 us
-    //                                       D 256: 299 / 192 / 273 us
-    //   32 sequences of 9 tokens (63 rows)  D 64:    - /  80 /  76 us
-    //                                       D 128:   - / 136 / 113 / 141 us
-    //                                       D 256:   - / 359 / 265 / 292 us
-    //   8 sequences of 64 tokens (448 rows) D 128:   - /   - / 163 / 155 us
-    //                                       D 256:   - /   - / 449 / 299 us
+    //   32 sequences of 4 tokens (28 rows)  D 64:   69 /  52 /  69 us
+    //                                       D 128: 126 /  93 / 104 us
+    //                                       D 256: 295 / 186 / 229 us
+    //   32 sequences of 9 tokens (63 rows)  D 64:    - /  78 /  73 us
+    //                                       D 128:   - / 136 / 112 / 134 us
+    //                                       D 256:   - / 345 / 249 / 308 us
+    //   8 sequences of 64 tokens (448 rows) D 128:   - /   - / 157 / 149 us
+    //                                       D 256:   - /   - / 413 / 339 us
     const int64_t rows = (T + B - 1) / B * (heads / kv_heads);
     p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D == 64 ? 64 : 128;
     // Four waves of up to 256 registers leave room for a second workgroup a compute
-    // unit (28 rows, 512 groups against 256: D 64 53 and 68 us, D 128 93 and 98 us); those
-    // of 64 rows and more have eight, D 256's use all registers (64 sequences of 1
-    // token: 287 us with 256, 299 with 512).
+    // unit; those of 64 rows and more have eight, D 256's use all registers.  Of 256
+    // and 512 groups:
+    //   32 sequences of 4 tokens (28 rows) over 8000   D 64:   66 /  52 us
+    //                                                  D 128:  97 /  93 us
+    //   64 sequences of 1 token over 8000              D 64:  107 /  83 us
+    //                                                  D 128: 149 / 149 us
+    //                                                  D 256: 283 / 295 us
+    //   4 sequences of 1 token over 8000               D 128:  20 /  22 us
+    //   1 sequence of 1 token over 30000               D 64:   16 /  17 us
+    // (few sequences, whose runs are then one unit long, lose by the rule)
     p.groups = D == 256 || p.rows >= 64 ? 256 : 512;
     p.part_floats = p.rows * (D + 2);
     p.bytes = p.groups * 2 * p.part_floats * 4;

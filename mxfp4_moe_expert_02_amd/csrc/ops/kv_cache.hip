@@ -4,9 +4,9 @@
 // element to the nearest E4M3 value; the block's four lanes agree on amax
 // through two quad exchanges.  Read: code * 2^scale.  Both move each byte
 // once and have next to no arithmetic: memory bounds them, and with few tokens
-// the launch (2.8 and 2.4 us).  16 bytes a thread in (write) or in and
+// the launch (2.9 and 2.4 us).  16 bytes a thread in (write) or in and
 // twice that out (read), whole cache lines a wave: 4096 tokens of 8 heads of
-// 128 elements are written in 8.2 us (25 MB, 3.1 TB/s), 16001 read in 17.8 us
+// 128 elements are written in 8.5 us (25 MB, 3.0 TB/s), 16001 read in 17.8 us
 // (99 MB, 5.6 TB/s).
 #include "attention_internal.h"
 

@@ -33,7 +33,7 @@
 //
 // With few rows the cache's bytes bound it: 32 sequences of 9 tokens and 56
 // heads (8 of keys) over up to 16384 positions of 128 elements take 178 us, 4.1 TB/s;
-// 64 of 1 token over up to 8000 of 64 elements 78 us, 4.3 TB/s.  With
+// 64 of 1 token over up to 8000 of 64 elements 77 us, 4.4 TB/s.  With
 // many it is the waves' own work: 8 trees of up to 64 tokens over up to 16001
 // positions take 141 us, 577 TFLOP/s.  Per tile a wave has 34 matrix
 // instructions (544 cycles), 16 exponentials (256), 88 other vector instructions
@@ -111,7 +111,16 @@ __device__ inline int wave_scan(int v) {
 // row tile costs about as much as 4 units (its queries, the first load, the
 // join): where it lets each row tile start a run of its own by at most 3 more
 // units a run, the line is laid out so, each row tile's units rounded up to
-// whole runs (1 sequence of 9 tokens over 8192 positions: 27 -> 20 us).
+// whole runs (1 sequence of 9 tokens over 8192 positions: 27 -> 20 us).  Past a
+// wave's lanes of sequences it is not tried, and both kernels' waves go through
+// the sequences 64 at a time, twice (1 token of 64 elements and 64 heads over up
+// to 2000 positions: 64 sequences 32 us, 65 33, 256 105, 1024 361).
+//
+// The line holds every unit of a sequence once for each row tile, also where no
+// mask is given and a tile's tokens see only up to their own position: of a
+// prompt's chunk without committed positions before it half of the units are
+// passed over unread (2048 tokens of 56 heads of 128: 316 us, 190 TFLOP/s; behind
+// 4096 positions 587, 512 TFLOP/s).
 struct Line {
     int total;   // units; 0 if the offsets are not ascending in 0 .. T
     int per;     // units of a workgroup
