@@ -124,9 +124,9 @@ int moe_kv_read(const moe_kv_rows_args* args, void* stream);
  *
  * Products and sums are float32's (of bf16 factors that hold q, k and v
  * exactly; a query or a cached value below 2^-126 may count as zero, one
- * beyond float32's range counts as infinite); the weights e^(s - m) are rounded to bf16 for
- * the product with v, and the sum they are divided by is that of the rounded
- * ones.  m is the running maximum as it last was where a score passed it by
+ * beyond float32's range counts as infinite); the weights e^(s - m) are
+ * rounded to bf16 for the product with v, and the sum they are divided by is
+ * that of the rounded ones.  m is the running maximum as it last was where a score passed it by
  * more than 8 powers of two.  Sums are added in an order that the sizes and
  * lengths decide: the same inputs give the same bits.  Scores that leave
  * float32's range give unspecified weights.

@@ -114,7 +114,9 @@ __device__ inline int wave_scan(int v) {
 // whole runs (1 sequence of 9 tokens over 8192 positions: 27 -> 20 us).  Past a
 // wave's lanes of sequences it is not tried, and both kernels' waves go through
 // the sequences 64 at a time, twice (1 token of 64 elements and 64 heads over up
-// to 2000 positions: 64 sequences 32 us, 65 33, 256 105, 1024 361).
+// to 2000 positions: 64 sequences 32 us, 65 33, 256 105, 1024 361).  That grows
+// with the square of their number (over up to 500 positions: 1024 sequences 0.2
+// ms, 4096 1.0, 16384 8.3, where the cache's bytes alone would take 0.8).
 //
 // The line holds every unit of a sequence once for each row tile, also where no
 // mask is given and a tile's tokens see only up to their own position: of a
